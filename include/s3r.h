@@ -18,6 +18,9 @@
  *   s3r_kv_rollback        back to the committed prefix after sampling
  *   s3r_verify_attn_tree   verification of a token tree (ancestor masks)
  *   s3r_tree_spec_sample   exact speculative sampling walked over the tree
+ *   s3r_kvq_append, _pack  a cache held in 4 or 8 bits, quantised as it is written
+ *   s3r_kvq_read           its rows back
+ *   s3r_kvq_attn           attention over it (draft rows and verification rows)
  *
  * Conventions shared by every call
  * --------------------------------
@@ -448,6 +451,136 @@ double s3r_round_cost_us(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, in
                          int32_t page_size, int32_t kv_bytes, double mean_context, int32_t budget_pages,
                          int32_t vocab, int32_t logit_bytes, int32_t gamma, double hbm_gbs,
                          double tensor_tflops);
+
+/*
+ * A paged KV cache held in 4 or 8 bits (the same paging as s3r_paged_kv). It
+ * serves as a second, smaller copy of the policy's cache that the drafter
+ * reads, or as the only cache. The S3R pages keep one cache in the model's
+ * type; this form has no counterpart there.
+ *
+ * A token's key (value) row x[0..D) of one KV head is held as whole numbers
+ * n_d in [0, 2^bits - 1] and two bf16 parameters, and stands for s n_d + z:
+ *   z = min_d x_d rounded down to bf16
+ *   s = bf16(float32((max_d x_d - z) / (2^bits - 1))), difference and quotient in float64
+ *   n_d = (x_d - z) / s (float64) rounded to the nearest whole number, ties to
+ *         even, at most 2^bits - 1
+ * A row whose s would be below 2^-100 (equal values) has s = 1 and n = 0. A row that
+ * holds NaN or an infinity has z = NaN: it reads back as NaN, and outputs of
+ * the attention rows that see it are NaN; rows that do not see it are not
+ * affected.
+ *
+ * pages: [num_pages_total, Hkv, s3r_kvq_page_bytes(D, P, bits)] bytes, base
+ *   16-byte aligned, of any content at first. The bytes of one (page, head):
+ *     K numbers  P*D*bits/8 bytes: [D*bits/128][P][16], byte j of piece c of
+ *                token t holds channels c*128/bits + j*8/bits ..., the lower
+ *                channel in the lower bits
+ *     K (s, z)   [P][2] bf16
+ *     V numbers  P*D*bits/8 bytes: [P*bits/8/u][D][u] with u = min(16, P*bits/8),
+ *                byte j of piece c of channel d holds tokens c*8u/bits + j*8/bits ...
+ *     V (s, z)   [P][2] bf16
+ * block_table, context_lens: as in s3r_paged_kv; the two may be shared with a
+ *   s3r_paged_kv of the same sequences. A page that several sequences list may be written
+ *   by one of them only, and in a call that no other sequence reads it in
+ *   (copy before writing).
+ */
+typedef struct {
+  int32_t num_seqs;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t max_pages_per_seq;
+  int32_t num_pages_total;
+  int32_t bits;                  /* 4 or 8 */
+  void* pages;
+  const int32_t* block_table;
+  const int32_t* context_lens;
+} s3r_paged_kvq;
+
+/* Bytes of one (page, head): 2 P D bits / 8 + 8 P. 0 for unsupported sizes. */
+size_t s3r_kvq_page_bytes(int32_t head_dim, int32_t page_size, int32_t bits);
+
+/*
+ * Rows quantised as they are written: for each sequence b the n rows
+ * k_new[b, t], v_new[b, t] go to positions L_b - overwrite + t (t < n).
+ * context_lens = kvq->context_lens: the length becomes L_b - overwrite + n (in
+ * place, as s3r_kv_append does). context_lens = NULL: the lengths stay as they are (for
+ * a copy that shares its lengths with another cache: call this first, then
+ * s3r_kv_append). Any other pointer is S3R_ERR_INVALID_ARG.
+ * k_new, v_new: [S, n, Hkv, D] in `dtype` (f32 or bf16), 16-byte aligned.
+ * 0 <= n, overwrite <= 1024; n = 0 with overwrite = 0 does nothing. Device
+ * checks as s3r_kv_append's: a sequence with overwrite > L_b or L_b -
+ * overwrite + n outside [1, max_pages_per_seq * P] is left unchanged
+ * (S3R_DEV_BAD_CONTEXT_LEN); a row whose page id is out of range is not
+ * written (S3R_DEV_BAD_PAGE_ID). Positions that are not written keep their
+ * bits. workspace: s3r_kv_workspace_bytes(num_seqs) bytes, zero-filled before
+ * first use.
+ */
+s3r_status s3r_kvq_append(const s3r_paged_kvq* kvq, int32_t* context_lens, const void* k_new, const void* v_new,
+                          s3r_dtype dtype, int32_t n, int32_t overwrite, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * Positions of an existing cache quantised: for each sequence of kv the last
+ * last_n positions (all of them for last_n = 0 or last_n >= L_b), under kv's lengths and block
+ * table, are written to the same positions of kvq under kvq's block table
+ * (kvq->context_lens is not read; it must not be NULL). The two caches agree in sequences, KV
+ * heads, head dim and page size (else S3R_ERR_INVALID_ARG). A length outside
+ * [1, max_pages_per_seq * P] of either cache leaves the sequence unchanged
+ * (S3R_DEV_BAD_CONTEXT_LEN); a page id out of range in either table skips the
+ * page (S3R_DEV_BAD_PAGE_ID). workspace: as s3r_kvq_append.
+ */
+s3r_status s3r_kvq_pack(const s3r_paged_kv* kv, const s3r_paged_kvq* kvq, int32_t last_n, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Rows read back: position start[b] + t (t < n) of sequence b to k_out[b, t],
+ * v_out[b, t], as s n + z rounded once to float32 and then to `dtype`. start:
+ * int32 [S] or NULL (0). Rows of positions >= L_b, of a sequence with start[b] < 0 or
+ * a bad length (S3R_DEV_BAD_CONTEXT_LEN) and of bad pages (S3R_DEV_BAD_PAGE_ID) are left
+ * as they were. k_out, v_out: [S, n, Hkv, D] in `dtype`, 16-byte aligned; n >= 0.
+ * workspace: as s3r_kvq_append (its status word).
+ */
+s3r_status s3r_kvq_read(const s3r_paged_kvq* kvq, const int32_t* start, int32_t n, s3r_dtype dtype, void* k_out,
+                        void* v_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The committed lengths after a round, as s3r_kv_rollback: L_b becomes L_b -
+ * rows + num_accepted[b] + 1 (context_lens must be kvq->context_lens). For a
+ * cache whose lengths are its own; a copy that shares its lengths with a
+ * s3r_paged_kv needs no call: s3r_kv_rollback moves the shared lengths.
+ * num_accepted[b] outside [0, rows - 1], or a length that would drop below 1,
+ * leaves the sequence unchanged (S3R_DEV_BAD_CONTEXT_LEN). 1 <= rows <= 17.
+ */
+s3r_status s3r_kvq_rollback(const s3r_paged_kvq* kvq, int32_t* context_lens, const int32_t* num_accepted, int32_t rows,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention over the quantised cache. Row r (0 <= r < rows) of sequence b sits
+ * at position L_b - rows + r and attends to the held keys and values k^ = s n
+ * + z of every position <= its own (rows = 1: a drafter's token; rows = gamma
+ * + 1: verification):
+ *   out[b,r,hq] = softmax(q[b,r,hq] k^^T * scale) v^, keys of KV head hq / G.
+ * page_list: NULL (every page), or int32 [S, Hkv, budget_pages] logical pages
+ *   to attend over, in any order, -1 for an unused entry (as `selected` of
+ *   s3r_sparse_draft_attn); a page listed twice counts twice; an entry outside [-1,
+ *   n_b) is skipped and flagged (S3R_DEV_BAD_PAGE_ID). budget_pages is 0
+ *   without a list, else 1 to 8192.
+ * A row that sees no position (only possible with a list) has out = 0 and lse
+ * = -inf, as have all rows of a sequence with L_b < rows, L_b < 1 or
+ * L_b > max_pages_per_seq * P (S3R_DEV_BAD_CONTEXT_LEN).
+ * q, out: [S, rows, Hq, D] in `dtype` (f32 or bf16), 16-byte aligned; lse:
+ *   float32 [S, rows, Hq] or NULL.
+ * Scores, softmax sums and outputs accumulate in float32. bf16: each weight
+ *   p s_v is rounded to bf16 before it meets the values' whole numbers.
+ * Supported as s3r_verify_attn: G <= 8, rows <= 17, G * rows <= 128.
+ * workspace: s3r_kvq_attn_workspace_bytes(kvq, dtype, rows, budget_pages)
+ *   bytes, zero-filled before first use.
+ */
+size_t s3r_kvq_attn_workspace_bytes(const s3r_paged_kvq* kvq, s3r_dtype dtype, int32_t rows, int32_t budget_pages);
+s3r_status s3r_kvq_attn(const s3r_paged_kvq* kvq, const void* q, s3r_dtype dtype, int32_t rows,
+                        const int32_t* page_list, int32_t budget_pages, float scale, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace sizes. Return 0 for an invalid or unsupported request.
  * Attention: rows = 1 and budget_pages > 0 for s3r_sparse_draft_attn;

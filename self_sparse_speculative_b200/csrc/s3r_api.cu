@@ -379,6 +379,159 @@ S3R_EXPORT s3r_status s3r_kv_rollback(const s3r_paged_kv* kv, int32_t* context_l
                                       static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------ quantised cache
+namespace {
+s3r_status check_kvq(const s3r_paged_kvq* c) {
+  if (!c) return S3R_ERR_INVALID_ARG;
+  if (c->num_seqs < 1 || c->num_q_heads < 1 || c->num_kv_heads < 1 || c->max_pages_per_seq < 1 || c->num_pages_total < 1)
+    return S3R_ERR_INVALID_ARG;
+  if (c->num_q_heads % c->num_kv_heads != 0) return S3R_ERR_INVALID_ARG;
+  if (!c->pages || !c->block_table || !c->context_lens || !aligned16(c->pages)) return S3R_ERR_INVALID_ARG;
+  if (c->bits != 4 && c->bits != 8) return S3R_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128) return S3R_ERR_UNSUPPORTED;
+  if (c->page_size != 16 && c->page_size != 64) return S3R_ERR_UNSUPPORTED;
+  if (c->num_q_heads / c->num_kv_heads > 8) return S3R_ERR_UNSUPPORTED;
+  if (c->max_pages_per_seq > kMaxPagesPerSeq) return S3R_ERR_UNSUPPORTED;
+  if ((uint64_t)c->num_pages_total * (uint64_t)c->num_kv_heads >= (1ull << 31)) return S3R_ERR_UNSUPPORTED;
+  if (c->num_seqs > 65535 || c->num_kv_heads > 65535) return S3R_ERR_UNSUPPORTED;       // grid y and z
+  return S3R_OK;
+}
+
+s3r_status check_kvq_call(const s3r_paged_kvq* c, const void* workspace, size_t workspace_bytes) {
+  s3r_status s = check_kvq(c);
+  if (s != S3R_OK) return s;
+  if (!workspace || workspace_bytes < kv_workspace_bytes(c->num_seqs)) return S3R_ERR_WORKSPACE;
+  return S3R_OK;
+}
+
+bool valid_dtype(s3r_dtype dt) { return dt == S3R_F32 || dt == S3R_BF16; }
+
+s3r_status check_kvq_attn(const s3r_paged_kvq* c, s3r_dtype dt, int32_t rows, int32_t budget) {
+  s3r_status s = check_kvq(c);
+  if (s != S3R_OK) return s;
+  if (!valid_dtype(dt) || rows < 1 || budget < 0) return S3R_ERR_INVALID_ARG;
+  const int G = c->num_q_heads / c->num_kv_heads;
+  if (rows > kMaxGamma + 1 || (int64_t)G * rows > 128) return S3R_ERR_UNSUPPORTED;
+  if (c->num_seqs > kMaxSeqs || budget > kMaxPagesPerSeq) return S3R_ERR_UNSUPPORTED;
+  // the flattened (sequence, KV head, page) list is walked with 32-bit positions
+  const int64_t pages = budget > 0 ? budget : c->max_pages_per_seq;
+  if ((int64_t)c->num_seqs * c->num_kv_heads * pages >= (1ll << 30)) return S3R_ERR_UNSUPPORTED;
+  return S3R_OK;
+}
+
+// The split plan of the attention kernels for this cache; a list may be longer than the block table is wide.
+AttnPlan plan_kvq_attention(const s3r_paged_kvq* c, int32_t rows, int32_t budget) {
+  s3r_paged_kv kv;
+  std::memset(&kv, 0, sizeof(kv));
+  kv.num_seqs = c->num_seqs;
+  kv.num_q_heads = c->num_q_heads;
+  kv.num_kv_heads = c->num_kv_heads;
+  kv.head_dim = c->head_dim;
+  kv.page_size = c->page_size;
+  kv.max_pages_per_seq = c->max_pages_per_seq > budget ? c->max_pages_per_seq : budget;
+  kv.num_pages_total = c->num_pages_total;
+  kv.dtype = S3R_F32;               // partial slots of the grid-split kernel, for both types
+  return plan_attention(kv, rows, budget);
+}
+}  // namespace
+
+S3R_EXPORT size_t s3r_kvq_page_bytes(int32_t head_dim, int32_t page_size, int32_t bits) {
+  if ((head_dim != 64 && head_dim != 128) || (page_size != 16 && page_size != 64) || (bits != 4 && bits != 8)) return 0;
+  return (size_t)(2 * (page_size * head_dim * bits / 8) + 8 * page_size);
+}
+
+S3R_EXPORT s3r_status s3r_kvq_append(const s3r_paged_kvq* kvq, int32_t* context_lens, const void* k_new,
+                                     const void* v_new, s3r_dtype dtype, int32_t n, int32_t overwrite, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  s3r_status s = check_kvq_call(kvq, workspace, workspace_bytes);
+  if (s != S3R_OK) return s;
+  if (!valid_dtype(dtype)) return S3R_ERR_INVALID_ARG;
+  if (context_lens && static_cast<const int32_t*>(context_lens) != kvq->context_lens) return S3R_ERR_INVALID_ARG;
+  if (n < 0 || overwrite < 0 || n > kMaxAppendRows || overwrite > kMaxAppendRows) return S3R_ERR_INVALID_ARG;
+  if (n > 0 && (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))) return S3R_ERR_INVALID_ARG;
+  if (n == 0 && (overwrite == 0 || !context_lens)) return S3R_OK;
+  return from_cuda(launch_kvq_append(*kvq, context_lens, k_new, v_new, dtype, n, overwrite, workspace,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+S3R_EXPORT s3r_status s3r_kvq_pack(const s3r_paged_kv* kv, const s3r_paged_kvq* kvq, int32_t last_n, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  s3r_status s = check_kv(kv);
+  if (s != S3R_OK) return s;
+  s = check_kvq_call(kvq, workspace, workspace_bytes);
+  if (s != S3R_OK) return s;
+  if (kv->num_seqs != kvq->num_seqs || kv->num_kv_heads != kvq->num_kv_heads || kv->head_dim != kvq->head_dim ||
+      kv->page_size != kvq->page_size || last_n < 0)
+    return S3R_ERR_INVALID_ARG;
+  return from_cuda(launch_kvq_pack(*kv, *kvq, last_n, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+S3R_EXPORT s3r_status s3r_kvq_read(const s3r_paged_kvq* kvq, const int32_t* start, int32_t n, s3r_dtype dtype, void* k_out,
+                                   void* v_out, void* workspace, size_t workspace_bytes, void* stream) {
+  s3r_status s = check_kvq_call(kvq, workspace, workspace_bytes);
+  if (s != S3R_OK) return s;
+  if (!valid_dtype(dtype) || n < 0) return S3R_ERR_INVALID_ARG;
+  if (n == 0) return S3R_OK;
+  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return S3R_ERR_INVALID_ARG;
+  return from_cuda(launch_kvq_read(*kvq, start, n, dtype, k_out, v_out, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+S3R_EXPORT s3r_status s3r_kvq_rollback(const s3r_paged_kvq* kvq, int32_t* context_lens, const int32_t* num_accepted,
+                                       int32_t rows, void* workspace, size_t workspace_bytes, void* stream) {
+  s3r_status s = check_kvq_call(kvq, workspace, workspace_bytes);
+  if (s != S3R_OK) return s;
+  if (!context_lens || static_cast<const int32_t*>(context_lens) != kvq->context_lens) return S3R_ERR_INVALID_ARG;
+  if (!num_accepted || rows < 1 || rows > kMaxGamma + 1) return S3R_ERR_INVALID_ARG;
+  return from_cuda(launch_kvq_rollback(*kvq, context_lens, num_accepted, rows, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+S3R_EXPORT size_t s3r_kvq_attn_workspace_bytes(const s3r_paged_kvq* kvq, s3r_dtype dtype, int32_t rows,
+                                               int32_t budget_pages) {
+  if (check_kvq_attn(kvq, dtype, rows, budget_pages) != S3R_OK) return 0;
+  return plan_kvq_attention(kvq, rows, budget_pages).ws_bytes;
+}
+
+S3R_EXPORT s3r_status s3r_kvq_attn(const s3r_paged_kvq* kvq, const void* q, s3r_dtype dtype, int32_t rows,
+                                   const int32_t* page_list, int32_t budget_pages, float scale, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  s3r_status s = check_kvq_attn(kvq, dtype, rows, budget_pages);
+  if (s != S3R_OK) return s;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || !std::isfinite(scale)) return S3R_ERR_INVALID_ARG;
+  if ((page_list != nullptr) != (budget_pages > 0)) return S3R_ERR_INVALID_ARG;
+  const AttnPlan pl = plan_kvq_attention(kvq, rows, budget_pages);
+  if (!workspace || workspace_bytes < pl.ws_bytes) return S3R_ERR_WORKSPACE;
+  KvqAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.pages = static_cast<const uint8_t*>(kvq->pages);
+  p.block_table = kvq->block_table;
+  p.context_lens = kvq->context_lens;
+  p.page_list = page_list;
+  p.S = kvq->num_seqs;
+  p.Hq = kvq->num_q_heads;
+  p.Hkv = kvq->num_kv_heads;
+  p.G = kvq->num_q_heads / kvq->num_kv_heads;
+  p.D = kvq->head_dim;
+  p.P = kvq->page_size;
+  p.R = rows;
+  p.rows = p.G * rows;
+  p.max_pages = kvq->max_pages_per_seq;
+  p.num_pages_total = kvq->num_pages_total;
+  p.budget = budget_pages;
+  p.nsplit = pl.nsplit;
+  p.chunk_pages = pl.chunk_pages;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  p.status = reinterpret_cast<uint32_t*>(w);
+  p.tickets = reinterpret_cast<uint32_t*>(w + pl.off_tickets);
+  p.part_ml = reinterpret_cast<float*>(w + pl.off_ml);
+  p.part_o = reinterpret_cast<float*>(w + pl.off_o);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return from_cuda(launch_kvq_attn_f32(*kvq, dtype, p, st));
+}
+
 S3R_EXPORT s3r_status s3r_debug_exp64(const double* x, double* y_tbl, double* y_ref, int32_t n, void* stream) {
   if (!x || !y_tbl || !y_ref || n < 1) return S3R_ERR_INVALID_ARG;
   return from_cuda(launch_exp64_probe(x, y_tbl, y_ref, n, static_cast<cudaStream_t>(stream)));

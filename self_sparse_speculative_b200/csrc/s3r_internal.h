@@ -142,6 +142,35 @@ cudaError_t launch_kv_append(const s3r_paged_kv& kv, int32_t* lens, const void* 
 cudaError_t launch_kv_rollback(const s3r_paged_kv& kv, int32_t* lens, const int32_t* num_accepted, int32_t rows,
                                void* kmin, void* kmax, void* ws, cudaStream_t st);
 
+// Quantised cache (s3r_kvq.cu): writing, reading back, rollback.
+cudaError_t launch_kvq_append(const s3r_paged_kvq& c, int32_t* lens, const void* k_new, const void* v_new, s3r_dtype dt,
+                              int32_t n, int32_t overwrite, void* ws, cudaStream_t st);
+cudaError_t launch_kvq_pack(const s3r_paged_kv& kv, const s3r_paged_kvq& c, int32_t last_n, void* ws, cudaStream_t st);
+cudaError_t launch_kvq_read(const s3r_paged_kvq& c, const int32_t* start, int32_t n, s3r_dtype dt, void* k_out, void* v_out,
+                            void* ws, cudaStream_t st);
+cudaError_t launch_kvq_rollback(const s3r_paged_kvq& c, int32_t* lens, const int32_t* num_accepted, int32_t rows, void* ws,
+                                cudaStream_t st);
+
+struct KvqAttnParams {
+  const void* q;              // [S, R, Hq, D]
+  void* out;
+  float* lse;                 // [S, R, Hq] or null
+  const uint8_t* pages;       // [num_pages_total, Hkv, page_bytes]
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  const int32_t* page_list;   // [S, Hkv, budget] logical pages (-1: none), or null: every page
+  int32_t S, Hq, Hkv, G, D, P, R;
+  int32_t r0, rows;           // first row of this launch, its packed rows (G x rows of the launch)
+  int32_t max_pages, num_pages_total, budget;
+  int32_t nsplit, chunk_pages;   // f32: grid splits per unit and pages per split
+  float scale_log2;              // scale * log2(e)
+  uint32_t* status;
+  uint32_t* tickets;             // [S * Hkv]
+  float* part_ml;                // [slots, rows, 2]
+  float* part_o;                 // [slots, rows, D]
+};
+cudaError_t launch_kvq_attn_f32(const s3r_paged_kvq& c, s3r_dtype dt, const KvqAttnParams& p, cudaStream_t st);
+
 struct SamplePlan {
   int32_t nrows;        // rows with statistics (2*gamma+1 per sequence, or num_rows)
   int32_t nseq;         // sequences (or rows for plain sampling)

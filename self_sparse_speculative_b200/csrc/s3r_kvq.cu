@@ -1,0 +1,509 @@
+// Writing and reading the quantised paged KV cache (layout and arithmetic of a
+// row: s3r_kvq.cuh). The drafter and the verifier of S3R share one cache
+// ("S3R: Fast and Faithful RL Rollouts via Self-Sparse Speculative Decoding",
+// weekinpapers.com, Abstract); held in 4 bits it is 3.8 times smaller than in
+// bf16, in 8 bits 1.9 times (D = 128).
+//
+//   kvq_store_kernel     rows quantised and written: n new rows per sequence
+//                        (append), or positions of a bf16 / f32 paged cache
+//                        (pack)
+//   kvq_read_kernel      a window of positions back to rows of bf16 / f32
+//   kvq_rollback_kernel  the lengths back to the committed prefix
+//
+// All are bound by HBM at length and by a chain of dependent loads (length ->
+// page id -> rows) for single rows. A CTA of 128 threads takes one tile of T
+// consecutive tokens of one (sequence, KV head), T = 32 for 64-token pages
+// and 16 for 16-token ones: a tile then holds whole V pieces, so the V bytes
+// of a tile belong to one CTA and no two CTAs of a call write the same byte.
+// A row is D/8 lanes of 8 channels (16-byte loads of bf16); minimum and maximum meet
+// by shuffles. K numbers go out as they are; V numbers turn channel-major
+// through shared memory, four channels by eight tokens per thread with byte
+// permutes, and leave as 16-byte pieces. A V piece of which only some tokens
+// are written keeps the other tokens' bits.
+//
+// These kernels write inputs of later calls: they wait for the previous kernel
+// before touching anything and let the next one start only when they are done.
+#include <cuda_bf16.h>
+
+#include "s3r_device.cuh"
+#include "s3r_internal.h"
+#include "s3r_kvq.cuh"
+
+namespace s3r {
+namespace {
+
+constexpr int kKvqThreads = 128;
+
+struct KvqParams {
+  uint8_t* pages;             // [num_pages_total, Hkv, page_bytes]
+  const int32_t* block_table;
+  const int32_t* lens;
+  int32_t* lens_out;          // append: lengths to update (null: leave them)
+  const void* k_src;          // append: rows [S, n, Hkv, D]; pack: paged cache [src_pages, Hkv, P, D]
+  const void* v_src;
+  const int32_t* src_table;   // pack: the source's block table
+  int32_t src_max_pages, src_pages_total;
+  void* k_out;                // read: [S, n, Hkv, D]
+  void* v_out;
+  const int32_t* start;       // read: first position per sequence (null: 0)
+  const int32_t* num_accepted;
+  int32_t S, Hkv, P, max_pages, num_pages_total;
+  int32_t n, overwrite, rows;
+  uint32_t* status;
+  uint32_t* tickets;          // [S]
+};
+
+// 8 consecutive channels of a row as floats.
+template <typename T> __device__ __forceinline__ void load8(const T* p, float* x);
+template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
+  const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <> __device__ __forceinline__ void load8<float>(const float* p, float* x) {
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+template <typename T> __device__ __forceinline__ void store8(T* p, const float* x);
+template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                            pack_bf16x2(x[6], x[7]));
+}
+template <> __device__ __forceinline__ void store8<float>(float* p, const float* x) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Rows x[k] (the 8 channels of this lane in each of NR rows): parameters (in
+// every lane of the row) and numbers, byte b of code[k] = channel b.
+template <int D, int BITS, int NR>
+__device__ __forceinline__ void quantise_rows(const float (*x)[8], uint32_t (*code)[2], uint32_t* param) {
+  float mn[NR], mx[NR];
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    mn[k] = mx[k] = x[k][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      mn[k] = min_nan(mn[k], x[k][i]);
+      mx[k] = max_nan(mx[k], x[k][i]);
+    }
+  }
+#pragma unroll
+  for (int o = D / 16; o >= 1; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      mn[k] = min_nan(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], o));
+      mx[k] = max_nan(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+    }
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    const KvqRow r = kvq_row<BITS>(mn[k], mx[k]);
+    param[k] = pack_bf16x2(r.s, r.z);
+    code[k][0] = code[k][1] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) code[k][i >> 2] |= kvq_number<BITS>(x[k][i], r) << (8 * (i & 3));
+  }
+}
+
+// Shared V numbers of a tile, a byte each: [T][D], rows padded so that the
+// four token groups of a warp fall on different banks.
+template <int D>
+constexpr int kVStride = D + 4;
+
+// V pieces of a tile: [T / ut][D] slots of 16 bytes, slot d at d ^ (d / 8 % 8)
+// of its group of eight.
+__device__ __forceinline__ int v_slot(int d) { return (d & ~7) | ((d ^ (d >> 3)) & 7); }
+
+// 4x4 byte transpose: byte c of in[r] -> byte r of out[c].
+__device__ __forceinline__ void transpose4(const uint32_t* in, uint32_t* out) {
+  const uint32_t a = __byte_perm(in[0], in[1], 0x5140), b = __byte_perm(in[0], in[1], 0x7362);
+  const uint32_t c = __byte_perm(in[2], in[3], 0x5140), d = __byte_perm(in[2], in[3], 0x7362);
+  out[0] = __byte_perm(a, c, 0x5410);
+  out[1] = __byte_perm(a, c, 0x7632);
+  out[2] = __byte_perm(b, d, 0x5410);
+  out[3] = __byte_perm(b, d, 0x7632);
+}
+
+// Bits of word w of a V piece (of `ut` tokens) whose tokens lie in [t0, t1).
+template <int BITS>
+__device__ __forceinline__ uint32_t token_mask(int w, int t0, int t1) {
+  constexpr int kPer = 32 / BITS;
+  const int a = max(0, min(kPer, t0 - w * kPer)) * BITS, b = max(0, min(kPer, t1 - w * kPer)) * BITS;
+  const uint32_t below_b = b >= 32 ? ~0u : (1u << b) - 1u, below_a = a >= 32 ? ~0u : (1u << a) - 1u;
+  return below_b & ~below_a;
+}
+
+template <typename T, int D, int P, int BITS, bool PACK>
+__global__ void __launch_bounds__(kKvqThreads) kvq_store_kernel(const KvqParams p) {
+  constexpr KvqLayout Y = kvq_layout(D, P, BITS);
+  constexpr int TT = P == 64 ? 32 : 16;                  // tokens per tile
+  constexpr int kLanes = D / 8;                          // lanes per row
+  constexpr int kRowsPass = kKvqThreads / kLanes;        // rows per pass of the CTA
+  constexpr int NR = TT / kRowsPass;                     // rows per lane: 4 or 2, or 1
+  constexpr int kPieces = TT / Y.ut;                     // V pieces per channel in a tile
+  constexpr int kWords = Y.unit / 4;                     // words per V piece
+  __shared__ __align__(16) uint32_t s_v[TT * kVStride<D> / 4];
+  __shared__ __align__(16) uint4 s_piece[kPieces * D];
+  pdl_wait();
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int L = __ldcg(p.lens + b);
+  int first, end;                                        // positions written
+  bool bad;
+  if (PACK) {
+    end = L;
+    first = p.n > 0 ? max(0, L - p.n) : 0;
+    bad = L < 1 || L > p.max_pages * P || L > p.src_max_pages * P;
+  } else {
+    first = L - p.overwrite;
+    end = first + p.n;
+    bad = L < 0 || first < 0 || end < 1 || end > p.max_pages * P;
+  }
+  if (bad) {
+    if (tid == 0 && h == 0 && blockIdx.x == 0) flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
+  } else {
+    const int tile = first / TT + blockIdx.x;
+    const int base = tile * TT;                          // first position of the tile
+    if (base < end && first < end) {
+      const int page = base / P, in_page = base - page * P;
+      const int phys = p.block_table[(size_t)b * p.max_pages + page];
+      bool ok = phys >= 0 && phys < p.num_pages_total;
+      int src = 0;
+      if (PACK) {
+        src = p.src_table[(size_t)b * p.src_max_pages + page];
+        ok = ok && src >= 0 && src < p.src_pages_total;
+      }
+      if (!ok) {
+        if (tid == 0) flag_status(p.status, S3R_DEV_BAD_PAGE_ID);
+      } else {
+        uint8_t* pg = p.pages + ((size_t)phys * p.Hkv + h) * Y.page_bytes;
+        const int row0 = tid / kLanes, c8 = tid % kLanes;
+        const int t0 = max(first - base, 0), t1 = min(end - base, TT);   // tokens of the tile written
+        float xk[NR][8], xv[NR][8];
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+          const int t = row0 + k * kRowsPass;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) xk[k][i] = xv[k][i] = 0.f;
+          if (t >= t0 && t < t1) {
+            const size_t at = PACK ? (((size_t)src * p.Hkv + h) * P + in_page + t) * D + c8 * 8
+                                   : (((size_t)b * p.n + (base + t - first)) * p.Hkv + h) * D + c8 * 8;
+            load8<T>(static_cast<const T*>(p.k_src) + at, xk[k]);
+            load8<T>(static_cast<const T*>(p.v_src) + at, xv[k]);
+          }
+        }
+        uint32_t code[NR][2], param[NR];
+        quantise_rows<D, BITS, NR>(xk, code, param);
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+          const int t = row0 + k * kRowsPass;
+          if (t < t0 || t >= t1) continue;
+          if (BITS == 4) {
+            // bytes (n0 n1 n2 n3) -> nibbles: (b | b >> 4) of each half-word
+            const uint32_t lo = code[k][0] | (code[k][0] >> 4), hi = code[k][1] | (code[k][1] >> 4);
+            *reinterpret_cast<uint32_t*>(pg + ((c8 >> 2) * P + in_page + t) * 16 + (c8 & 3) * 4) =
+                __byte_perm(lo, hi, 0x6420);
+          } else {
+            *reinterpret_cast<uint2*>(pg + ((c8 >> 1) * P + in_page + t) * 16 + (c8 & 1) * 8) =
+                make_uint2(code[k][0], code[k][1]);
+          }
+          if (c8 == 0) *reinterpret_cast<uint32_t*>(pg + Y.off_kp + (in_page + t) * 4) = param[k];
+        }
+        quantise_rows<D, BITS, NR>(xv, code, param);
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+          const int t = row0 + k * kRowsPass;
+          s_v[(t * kVStride<D>) / 4 + c8 * 2] = code[k][0];
+          s_v[(t * kVStride<D>) / 4 + c8 * 2 + 1] = code[k][1];
+          if (c8 == 0 && t >= t0 && t < t1)
+            *reinterpret_cast<uint32_t*>(pg + Y.off_vp + (in_page + t) * 4) = param[k];
+        }
+        __syncthreads();
+        // four channels x eight tokens per step: lanes take 8 channel groups x 4 token groups
+        constexpr int kTg = TT / 8;
+        for (int s = tid; s < (D / 4) * kTg; s += kKvqThreads) {
+          const int in = s % (8 * kTg), cg = (s / (8 * kTg)) * 8 + (in & 7), tg = in >> 3;
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[k] = s_v[((tg * 8 + k) * kVStride<D>) / 4 + cg];
+          uint32_t a[4], o[4];
+          if (BITS == 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a[k] = w[2 * k] | (w[2 * k + 1] << 4);
+            transpose4(a, o);
+            const int piece = tg * 8 / Y.ut, word = (tg * 8 % Y.ut) / 8;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              reinterpret_cast<uint32_t*>(&s_piece[piece * D + v_slot(cg * 4 + c)])[word] = o[c];
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              transpose4(w + 4 * q, o);
+              const int t = tg * 8 + 4 * q;
+              const int piece = t / Y.ut, word = (t % Y.ut) / 4;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                reinterpret_cast<uint32_t*>(&s_piece[piece * D + v_slot(cg * 4 + c)])[word] = o[c];
+            }
+          }
+        }
+        __syncthreads();
+        for (int s = tid; s < kPieces * D; s += kKvqThreads) {
+          const int piece = s / D, d = s - (s / D) * D;
+          const int u0 = piece * Y.ut;                   // first token of the piece, within the tile
+          const int a = t0 - u0, e = t1 - u0;
+          if (e <= 0 || a >= Y.ut) continue;
+          uint4 v = s_piece[piece * D + v_slot(d)];
+          uint8_t* dst = pg + Y.off_v + ((in_page / Y.ut + piece) * D + d) * Y.unit;
+          if (a > 0 || e < Y.ut) {                       // keep the other tokens' bits
+            uint32_t* nv = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+              const uint32_t m = token_mask<BITS>(w, a, e);
+              nv[w] = (nv[w] & m) | (reinterpret_cast<const uint32_t*>(dst)[w] & ~m);
+            }
+          }
+          if (Y.unit == 16) *reinterpret_cast<uint4*>(dst) = v;
+          else *reinterpret_cast<uint2*>(dst) = make_uint2(v.x, v.y);
+        }
+      }
+    }
+  }
+  if (!PACK && p.lens_out) {
+    // the last CTA of the sequence stores its new length
+    __syncthreads();
+    if (tid == 0) {
+      __threadfence();
+      if (atomicAdd(p.tickets + b, 1u) == gridDim.x * gridDim.y - 1u) {
+        if (!bad) p.lens_out[b] = end;
+        p.tickets[b] = 0u;
+      }
+    }
+  }
+}
+
+template <typename T, int D, int P, int BITS>
+__global__ void __launch_bounds__(kKvqThreads) kvq_read_kernel(const KvqParams p) {
+  constexpr KvqLayout Y = kvq_layout(D, P, BITS);
+  constexpr int TT = P == 64 ? 32 : 16;
+  constexpr int kLanes = D / 8;
+  constexpr int kRowsPass = kKvqThreads / kLanes;
+  constexpr int NR = TT / kRowsPass;
+  constexpr int kPieces = TT / Y.ut;
+  __shared__ __align__(16) uint32_t s_v[TT * kVStride<D> / 4];
+  __shared__ __align__(16) uint4 s_piece[kPieces * D];
+  pdl_wait();
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int L = __ldcg(p.lens + b);
+  const int first = p.start ? __ldcg(p.start + b) : 0;
+  if (L < 1 || L > p.max_pages * P || first < 0) {
+    if (tid == 0 && h == 0 && blockIdx.x == 0) flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
+    return;
+  }
+  const int end = p.n < L - first ? first + p.n : L;     // rows of positions >= L are left as they are
+  const int base = (first / TT + (int)blockIdx.x) * TT;
+  if (base >= end || first >= end) return;
+  const int page = base / P, in_page = base - page * P;
+  const int phys = p.block_table[(size_t)b * p.max_pages + page];
+  if (phys < 0 || phys >= p.num_pages_total) {
+    if (tid == 0) flag_status(p.status, S3R_DEV_BAD_PAGE_ID);
+    return;
+  }
+  const uint8_t* pg = p.pages + ((size_t)phys * p.Hkv + h) * Y.page_bytes;
+  const int row0 = tid / kLanes, c8 = tid % kLanes;
+  const int t0 = max(first - base, 0), t1 = min(end - base, TT);
+  // every load of the tile first
+  for (int s = tid; s < kPieces * D; s += kKvqThreads) {
+    const int piece = s / D, d = s - (s / D) * D;
+    const uint8_t* src = pg + Y.off_v + ((in_page / Y.ut + piece) * D + d) * Y.unit;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (Y.unit == 16) v = __ldcg(reinterpret_cast<const uint4*>(src));
+    else {
+      const uint2 a = __ldcg(reinterpret_cast<const uint2*>(src));
+      v.x = a.x;
+      v.y = a.y;
+    }
+    s_piece[piece * D + v_slot(d)] = v;
+  }
+  uint2 kc[NR];
+  uint32_t kp[NR], vp[NR];
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    const int t = in_page + row0 + k * kRowsPass;
+    if (BITS == 4) kc[k].x = __ldcg(reinterpret_cast<const uint32_t*>(pg + ((c8 >> 2) * P + t) * 16 + (c8 & 3) * 4));
+    else kc[k] = __ldcg(reinterpret_cast<const uint2*>(pg + ((c8 >> 1) * P + t) * 16 + (c8 & 1) * 8));
+    kp[k] = __ldcg(reinterpret_cast<const uint32_t*>(pg + Y.off_kp + t * 4));
+    vp[k] = __ldcg(reinterpret_cast<const uint32_t*>(pg + Y.off_vp + t * 4));
+  }
+  auto put = [&](void* out, int t, uint32_t lo, uint32_t hi, uint32_t par) {
+    // bytes of lo, hi: the 8 channels' numbers
+    const float s = __uint_as_float(par << 16), z = __uint_as_float(par & 0xffff0000u);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t n = ((i < 4 ? lo : hi) >> (8 * (i & 3))) & 0xffu;
+      x[i] = fmaf(s, __uint_as_float(0x4b000000u | n) - 8388608.f, z);
+    }
+    store8<T>(static_cast<T*>(out) + (((size_t)b * p.n + (base + t - first)) * p.Hkv + h) * D + c8 * 8, x);
+  };
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    const int t = row0 + k * kRowsPass;
+    if (t < t0 || t >= t1) continue;
+    if (BITS == 4) {
+      const uint32_t e = kc[k].x & 0x0f0f0f0fu, o = (kc[k].x >> 4) & 0x0f0f0f0fu;   // even, odd channels
+      put(p.k_out, t, __byte_perm(e, o, 0x5140), __byte_perm(e, o, 0x7362), kp[k]);
+    } else {
+      put(p.k_out, t, kc[k].x, kc[k].y, kp[k]);
+    }
+  }
+  __syncthreads();
+  constexpr int kTg = TT / 8;
+  for (int s = tid; s < (D / 4) * kTg; s += kKvqThreads) {
+    const int in = s % (8 * kTg), cg = (s / (8 * kTg)) * 8 + (in & 7), tg = in >> 3;
+    uint32_t a[4], o[4];
+    if (BITS == 4) {
+      const int piece = tg * 8 / Y.ut, word = (tg * 8 % Y.ut) / 8;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        a[c] = reinterpret_cast<const uint32_t*>(&s_piece[piece * D + v_slot(cg * 4 + c)])[word];
+      transpose4(a, o);                                  // o[k]: tokens 2k, 2k+1 of four channels
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s_v[((tg * 8 + 2 * k) * kVStride<D>) / 4 + cg] = o[k] & 0x0f0f0f0fu;
+        s_v[((tg * 8 + 2 * k + 1) * kVStride<D>) / 4 + cg] = (o[k] >> 4) & 0x0f0f0f0fu;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int t = tg * 8 + 4 * q;
+        const int piece = t / Y.ut, word = (t % Y.ut) / 4;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          a[c] = reinterpret_cast<const uint32_t*>(&s_piece[piece * D + v_slot(cg * 4 + c)])[word];
+        transpose4(a, o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s_v[((t + k) * kVStride<D>) / 4 + cg] = o[k];
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    const int t = row0 + k * kRowsPass;
+    if (t < t0 || t >= t1) continue;
+    put(p.v_out, t, s_v[(t * kVStride<D>) / 4 + c8 * 2], s_v[(t * kVStride<D>) / 4 + c8 * 2 + 1], vp[k]);
+  }
+}
+
+__global__ void __launch_bounds__(kKvqThreads) kvq_rollback_kernel(const KvqParams p) {
+  pdl_wait();
+  const int b = blockIdx.x * kKvqThreads + threadIdx.x;
+  if (b >= p.S) return;
+  const int L = p.lens_out[b], nacc = p.num_accepted[b];
+  const int new_len = L - p.rows + nacc + 1;
+  if (nacc < 0 || nacc >= p.rows || new_len < 1 || L > p.max_pages * p.P) {
+    flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
+    return;
+  }
+  p.lens_out[b] = new_len;
+}
+
+KvqParams base_params(const s3r_paged_kvq& c, void* ws) {
+  KvqParams p{};
+  p.pages = static_cast<uint8_t*>(c.pages);
+  p.block_table = c.block_table;
+  p.lens = c.context_lens;
+  p.S = c.num_seqs;
+  p.Hkv = c.num_kv_heads;
+  p.P = c.page_size;
+  p.max_pages = c.max_pages_per_seq;
+  p.num_pages_total = c.num_pages_total;
+  p.status = static_cast<uint32_t*>(ws);
+  p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kWsHeader);
+  return p;
+}
+
+// Tiles of TT tokens that n consecutive positions may touch.
+int tiles_of(int n, int P) {
+  const int tt = P == 64 ? 32 : 16;
+  return n <= 0 ? 1 : (n + tt - 2) / tt + 1;
+}
+
+enum KvqOp { kStoreRows, kStorePages, kRead };
+
+template <typename T, int D, int P, int BITS>
+cudaError_t launch_one(KvqOp op, const KvqParams& p, dim3 grid, cudaStream_t st) {
+  const dim3 block(kKvqThreads);
+  switch (op) {
+    case kStoreRows: return launch_kernel(kvq_store_kernel<T, D, P, BITS, false>, grid, block, 0, st, 1, p);
+    case kStorePages: return launch_kernel(kvq_store_kernel<T, D, P, BITS, true>, grid, block, 0, st, 1, p);
+    default: return launch_kernel(kvq_read_kernel<T, D, P, BITS>, grid, block, 0, st, 1, p);
+  }
+}
+template <typename T, int D, int P>
+cudaError_t launch_bits(KvqOp op, int bits, const KvqParams& p, dim3 grid, cudaStream_t st) {
+  return bits == 4 ? launch_one<T, D, P, 4>(op, p, grid, st) : launch_one<T, D, P, 8>(op, p, grid, st);
+}
+template <typename T>
+cudaError_t launch_shape(KvqOp op, const s3r_paged_kvq& c, const KvqParams& p, dim3 grid, cudaStream_t st) {
+  if (c.head_dim == 64)
+    return c.page_size == 16 ? launch_bits<T, 64, 16>(op, c.bits, p, grid, st) : launch_bits<T, 64, 64>(op, c.bits, p, grid, st);
+  return c.page_size == 16 ? launch_bits<T, 128, 16>(op, c.bits, p, grid, st) : launch_bits<T, 128, 64>(op, c.bits, p, grid, st);
+}
+cudaError_t launch_typed(KvqOp op, s3r_dtype dt, const s3r_paged_kvq& c, const KvqParams& p, dim3 grid, cudaStream_t st) {
+  return dt == S3R_BF16 ? launch_shape<__nv_bfloat16>(op, c, p, grid, st) : launch_shape<float>(op, c, p, grid, st);
+}
+
+}  // namespace
+
+cudaError_t launch_kvq_append(const s3r_paged_kvq& c, int32_t* lens, const void* k_new, const void* v_new, s3r_dtype dt,
+                              int32_t n, int32_t overwrite, void* ws, cudaStream_t st) {
+  KvqParams p = base_params(c, ws);
+  p.lens_out = lens;
+  p.k_src = k_new;
+  p.v_src = v_new;
+  p.n = n;
+  p.overwrite = overwrite;
+  return launch_typed(kStoreRows, dt, c, p, dim3(tiles_of(n, c.page_size), c.num_kv_heads, c.num_seqs), st);
+}
+
+cudaError_t launch_kvq_pack(const s3r_paged_kv& kv, const s3r_paged_kvq& c, int32_t last_n, void* ws, cudaStream_t st) {
+  KvqParams p = base_params(c, ws);
+  p.lens = kv.context_lens;
+  p.k_src = kv.k_cache;
+  p.v_src = kv.v_cache;
+  p.src_table = kv.block_table;
+  p.src_max_pages = kv.max_pages_per_seq;
+  p.src_pages_total = kv.num_pages_total;
+  p.n = last_n;
+  const int cap = (c.max_pages_per_seq < kv.max_pages_per_seq ? c.max_pages_per_seq : kv.max_pages_per_seq) * c.page_size;
+  const int n = last_n > 0 && last_n < cap ? last_n : cap;
+  return launch_typed(kStorePages, kv.dtype, c, p, dim3(tiles_of(n, c.page_size), c.num_kv_heads, c.num_seqs), st);
+}
+
+cudaError_t launch_kvq_read(const s3r_paged_kvq& c, const int32_t* start, int32_t n, s3r_dtype dt, void* k_out, void* v_out,
+                            void* ws, cudaStream_t st) {
+  KvqParams p = base_params(c, ws);
+  p.start = start;
+  p.n = n;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  const int cap = c.max_pages_per_seq * c.page_size;
+  return launch_typed(kRead, dt, c, p, dim3(tiles_of(n < cap ? n : cap, c.page_size), c.num_kv_heads, c.num_seqs), st);
+}
+
+cudaError_t launch_kvq_rollback(const s3r_paged_kvq& c, int32_t* lens, const int32_t* num_accepted, int32_t rows, void* ws,
+                                cudaStream_t st) {
+  KvqParams p = base_params(c, ws);
+  p.lens_out = lens;
+  p.num_accepted = num_accepted;
+  p.rows = rows;
+  return launch_kernel(kvq_rollback_kernel, dim3((c.num_seqs + kKvqThreads - 1) / kKvqThreads), dim3(kKvqThreads), 0, st, 1, p);
+}
+
+}  // namespace s3r

@@ -1,0 +1,113 @@
+// The quantised paged KV cache: where the bytes of one (page, head) lie, and
+// the arithmetic of a row's parameters.
+//
+// A token row x[0..D) of a head is held as whole numbers n_d of `bits` bits
+// and two bf16 parameters, and stands for s n_d + z:
+//   z = min x rounded down to bf16,  s = bf16(float32((max x - z) / (2^bits - 1)))
+//   n_d = (x_d - z) / s rounded to the nearest, ties to even (float64 quotient)
+// One scale per token and head (not per page and channel) lets a row be
+// written the moment it exists: no other row of the page changes. z is
+// rounded down so that no n_d is negative; n_d above 2^bits - 1 (s rounded
+// down) is clamped, which moves it by at most 2^-8 of the row's range.
+//
+// One (page, head) is one contiguous run of bytes, so that one bulk copy
+// fetches it:
+//   K numbers  [D*bits/128][P][16 B]  channel pieces of 16 bytes, token by token
+//   K (s, z)   [P][2] bf16
+//   V numbers  [P*bits/8/u][D][u B]   u = min(16, P*bits/8): token pieces, channel by channel
+//   V (s, z)   [P][2] bf16
+// The keys lie token-major and the values channel-major: attention's two
+// contractions run over channels (q k) and over tokens (p v), and each of its
+// threads unpacks one row of its operand from 16-byte pieces that neighbouring
+// threads read from neighbouring addresses.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "s3r.h"
+
+namespace s3r {
+
+constexpr float kKvqTiny = 7.888609052210118e-31f;   // 2^-100: rows of a smaller step are held flat (s = 1, n = 0)
+
+struct KvqLayout {
+  int half;      // bytes of one side's numbers, P * D * bits / 8
+  int unit;      // bytes of one V piece
+  int ut;        // tokens of one V piece
+  int off_kp, off_v, off_vp, page_bytes;
+};
+__host__ __device__ constexpr KvqLayout kvq_layout(int D, int P, int bits) {
+  KvqLayout l{};
+  l.half = P * D * bits / 8;
+  l.unit = P * bits / 8 < 16 ? P * bits / 8 : 16;
+  l.ut = l.unit * 8 / bits;
+  l.off_kp = l.half;
+  l.off_v = l.half + 4 * P;
+  l.off_vp = 2 * l.half + 4 * P;
+  l.page_bytes = 2 * l.half + 8 * P;
+  return l;
+}
+
+struct KvqRow {
+  float z, s, inv;   // parameters (bf16 values) and 1 / s
+  bool flat;         // every n is 0
+};
+
+// min and max that keep a NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Parameters of a row with minimum mn and maximum mx (either NaN if the row
+// holds one). The float32 quotient is off by at most 2^-23 of itself, so it
+// decides the bf16 rounding unless it lies within a few steps of a midpoint;
+// there, and where max - z overflows, the float64 quotient is taken.
+template <int BITS>
+__device__ __forceinline__ KvqRow kvq_row(float mn, float mx) {
+  constexpr int kTop = (1 << BITS) - 1;
+  KvqRow r;
+  r.flat = true;
+  r.s = 1.f;
+  r.inv = 1.f;
+  if (!(mn > -INFINITY && mx < INFINITY)) {            // NaN or infinity in the row
+    r.z = __int_as_float(0x7fc00000);
+    return r;
+  }
+  r.z = __bfloat162float(__float2bfloat16_rd(mn));
+  const float range = mx - r.z;
+  float q = __fdiv_rn(range, (float)kTop);
+  const uint32_t low = __float_as_uint(q) & 0xffffu;
+  if (!(range < INFINITY) || (low > 0x7ff8u && low < 0x8008u)) q = (float)(((double)mx - (double)r.z) / kTop);
+  const float s = __bfloat162float(__float2bfloat16_rn(q));
+  if (s < kKvqTiny) return r;
+  r.flat = false;
+  r.s = s;
+  r.inv = __frcp_rn(s);
+  return r;
+}
+
+// n of x. The float32 product is within 255 * 2^-22 of the quotient; nearer
+// than 2^-12 to a rounding border, or where x - z overflows, the float64
+// quotient decides.
+template <int BITS>
+__device__ __forceinline__ uint32_t kvq_number(float x, const KvqRow& r) {
+  constexpr int kTop = (1 << BITS) - 1;
+  if (r.flat) return 0u;
+  const float t = (x - r.z) * r.inv;
+  const float f = t + 12582912.f;                        // 1.5 * 2^23: rounds to the nearest whole, ties to even
+  int n = (int)(__float_as_uint(f) & 0x3fffffu);
+  const float d = t - (f - 12582912.f);
+  if (!(fabsf(d) <= 0.5f - 0.000244140625f)) n = __double2int_rn(((double)x - (double)r.z) / (double)r.s);
+  return (uint32_t)(n < kTop ? n : kTop);
+}
+
+}  // namespace s3r

@@ -28,6 +28,8 @@ EXPORTED = [
     "s3r_debug_exp64", "s3r_gamma_policy_init", "s3r_gamma_policy_update", "s3r_gamma_policy_choose",
     "s3r_attend_cost_us", "s3r_round_cost_us", "s3r_verify_attn_tree", "s3r_tree_spec_sample",
     "s3r_tree_sample_workspace_bytes", "s3r_tree_node_budget",
+    "s3r_kvq_page_bytes", "s3r_kvq_append", "s3r_kvq_pack", "s3r_kvq_read", "s3r_kvq_rollback",
+    "s3r_kvq_attn_workspace_bytes", "s3r_kvq_attn",
 ]
 
 
@@ -52,12 +54,21 @@ class PagedKV(ctypes.Structure):
     ]
 
 
+class PagedKVQ(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+        ("num_pages_total", ctypes.c_int32), ("bits", ctypes.c_int32),
+        ("pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libs3r.so is not built ({LIB_PATH}); run python -m self_sparse_speculative_b200.build")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, f32, sz, f64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t, ctypes.c_double
-    kvp = ctypes.POINTER(PagedKV)
+    kvp, kqp = ctypes.POINTER(PagedKV), ctypes.POINTER(PagedKVQ)
     sig = {
         "s3r_page_summaries": ([kvp, i32, vp, vp, vp], i32),
         "s3r_page_summaries_checked": ([kvp, i32, vp, vp, vp, vp], i32),
@@ -88,6 +99,13 @@ def _load():
         "s3r_tree_sample_workspace_bytes": ([i32, i32, i32], sz),
         "s3r_tree_spec_sample": ([vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, sz, vp], i32),
         "s3r_tree_node_budget": ([ctypes.c_int64, i32, i32, i32], i32),
+        "s3r_kvq_page_bytes": ([i32, i32, i32], sz),
+        "s3r_kvq_append": ([kqp, vp, vp, vp, i32, i32, i32, vp, sz, vp], i32),
+        "s3r_kvq_pack": ([kvp, kqp, i32, vp, sz, vp], i32),
+        "s3r_kvq_read": ([kqp, vp, i32, i32, vp, vp, vp, sz, vp], i32),
+        "s3r_kvq_rollback": ([kqp, vp, vp, i32, vp, sz, vp], i32),
+        "s3r_kvq_attn_workspace_bytes": ([kqp, i32, i32, i32], sz),
+        "s3r_kvq_attn": ([kqp, vp, i32, i32, vp, i32, f32, vp, vp, vp, sz, vp], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -289,6 +307,108 @@ def s3r_kv_rollback(kv: PagedKV, context_lens, num_accepted, rows: int, kmin, km
     st = _lib.s3r_kv_rollback(ctypes.byref(kv), _ptr(context_lens), _ptr(num_accepted), int(rows), _ptr(kmin),
                               _ptr(kmax), _ptr(workspace), wb, _stream(stream))
     _check("s3r_kv_rollback", st)
+
+
+def s3r_kvq_page_bytes(head_dim: int, page_size: int, bits: int) -> int:
+    """Bytes of one (page, KV head) of a quantised cache; 0 for unsupported sizes."""
+    return int(_lib.s3r_kvq_page_bytes(int(head_dim), int(page_size), int(bits)))
+
+
+def _expect(name, x, dtype, shape):
+    """A tensor argument the library would read or write past if its type, shape or layout were another."""
+    if x is None or isinstance(x, int):
+        return
+    if tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {x.dtype} {tuple(x.shape)}")
+    if x.is_cuda:
+        import torch
+        if x.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} lives on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+    else:
+        raise ValueError(f"{name} must live on the GPU")
+
+
+def _torch_dtype(dtype):
+    import torch
+    return torch.bfloat16 if dtype_code(dtype) == S3R_BF16 else torch.float32
+
+
+def paged_kvq(pages, block_table, context_lens, num_q_heads: int, head_dim: int, page_size: int, bits: int) -> PagedKVQ:
+    """Describe a quantised cache: pages uint8 [num_pages_total, Hkv, s3r_kvq_page_bytes(D, P, bits)]."""
+    import torch
+    n, h, nb = pages.shape
+    if nb != s3r_kvq_page_bytes(head_dim, page_size, bits):
+        raise ValueError(f"pages have {nb} bytes per head, head_dim {head_dim}, page_size {page_size} and {bits} bits "
+                         f"need {s3r_kvq_page_bytes(head_dim, page_size, bits)}")
+    _expect("pages", pages, torch.uint8, (n, h, nb))
+    _expect("block_table", block_table, torch.int32, block_table.shape)
+    _expect("context_lens", context_lens, torch.int32, (block_table.shape[0],))
+    kvq = PagedKVQ(int(block_table.shape[0]), int(num_q_heads), int(h), int(head_dim), int(page_size),
+                   int(block_table.shape[1]), int(n), int(bits), _ptr(pages), _ptr(block_table), _ptr(context_lens))
+    kvq.tensors = (pages, block_table, context_lens)     # alive as long as the description
+    return kvq
+
+
+def s3r_kvq_append(kvq: PagedKVQ, context_lens, k_new, v_new, dtype, n: int, overwrite: int, workspace,
+                   workspace_bytes=None, stream=None):
+    """Quantise n rows per sequence into positions L - overwrite.. (updating L; context_lens None: L stays)."""
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    shape = (kvq.num_seqs, n, kvq.num_kv_heads, kvq.head_dim)
+    _expect("k_new", k_new, _torch_dtype(dtype), shape)
+    _expect("v_new", v_new, _torch_dtype(dtype), shape)
+    st = _lib.s3r_kvq_append(ctypes.byref(kvq), _ptr(context_lens), _ptr(k_new), _ptr(v_new), dtype_code(dtype), int(n),
+                             int(overwrite), _ptr(workspace), wb, _stream(stream))
+    _check("s3r_kvq_append", st)
+
+
+def s3r_kvq_pack(kv: PagedKV, kvq: PagedKVQ, last_n: int, workspace, workspace_bytes=None, stream=None):
+    """Quantise the last last_n positions (0: all) of each sequence of kv into kvq."""
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    st = _lib.s3r_kvq_pack(ctypes.byref(kv), ctypes.byref(kvq), int(last_n), _ptr(workspace), wb, _stream(stream))
+    _check("s3r_kvq_pack", st)
+
+
+def s3r_kvq_read(kvq: PagedKVQ, start, n: int, dtype, k_out, v_out, workspace, workspace_bytes=None, stream=None):
+    """Positions start[b] + t (start None: 0) of each sequence to rows k_out[b, t], v_out[b, t]."""
+    import torch
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    shape = (kvq.num_seqs, n, kvq.num_kv_heads, kvq.head_dim)
+    _expect("start", start, torch.int32, (kvq.num_seqs,))
+    _expect("k_out", k_out, _torch_dtype(dtype), shape)
+    _expect("v_out", v_out, _torch_dtype(dtype), shape)
+    st = _lib.s3r_kvq_read(ctypes.byref(kvq), _ptr(start), int(n), dtype_code(dtype), _ptr(k_out), _ptr(v_out),
+                           _ptr(workspace), wb, _stream(stream))
+    _check("s3r_kvq_read", st)
+
+
+def s3r_kvq_rollback(kvq: PagedKVQ, context_lens, num_accepted, rows: int, workspace, workspace_bytes=None, stream=None):
+    """L <- L - rows + n_acc + 1."""
+    import torch
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _expect("num_accepted", num_accepted, torch.int32, (kvq.num_seqs,))
+    st = _lib.s3r_kvq_rollback(ctypes.byref(kvq), _ptr(context_lens), _ptr(num_accepted), int(rows), _ptr(workspace), wb,
+                               _stream(stream))
+    _check("s3r_kvq_rollback", st)
+
+
+def s3r_kvq_attn_workspace_bytes(kvq: PagedKVQ, dtype, rows: int, budget_pages: int = 0) -> int:
+    return int(_lib.s3r_kvq_attn_workspace_bytes(ctypes.byref(kvq), dtype_code(dtype), int(rows), int(budget_pages)))
+
+
+def s3r_kvq_attn(kvq: PagedKVQ, q, dtype, rows: int, scale: float, out, lse, workspace, pages=None, budget_pages: int = 0,
+                 workspace_bytes=None, stream=None):
+    """Causal attention of `rows` rows per sequence over the quantised cache (pages: the list of kept pages, or all)."""
+    import torch
+    wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    shape = (kvq.num_seqs, rows, kvq.num_q_heads, kvq.head_dim)
+    _expect("q", q, _torch_dtype(dtype), shape)
+    _expect("out", out, _torch_dtype(dtype), shape)
+    _expect("lse", lse, torch.float32, shape[:3])
+    _expect("pages", pages, torch.int32, (kvq.num_seqs, kvq.num_kv_heads, budget_pages))
+    st = _lib.s3r_kvq_attn(ctypes.byref(kvq), _ptr(q), dtype_code(dtype), int(rows), _ptr(pages), int(budget_pages),
+                           float(scale), _ptr(out), _ptr(lse), _ptr(workspace), wb, _stream(stream))
+    _check("s3r_kvq_attn", st)
 
 
 def s3r_debug_exp64(x, y_tbl, y_ref, stream=None):
