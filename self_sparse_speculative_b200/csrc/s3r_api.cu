@@ -419,8 +419,9 @@ s3r_status check_kvq_attn(const s3r_paged_kvq* c, s3r_dtype dt, int32_t rows, in
   return S3R_OK;
 }
 
-// The split plan of the attention kernels for this cache; a list may be longer than the block table is wide.
-AttnPlan plan_kvq_attention(const s3r_paged_kvq* c, int32_t rows, int32_t budget) {
+// The split plan of the attention kernels for this cache, with the type's
+// partial slots; a list may be longer than the block table is wide.
+AttnPlan plan_kvq_attention(const s3r_paged_kvq* c, s3r_dtype dt, int32_t rows, int32_t budget) {
   s3r_paged_kv kv;
   std::memset(&kv, 0, sizeof(kv));
   kv.num_seqs = c->num_seqs;
@@ -430,7 +431,7 @@ AttnPlan plan_kvq_attention(const s3r_paged_kvq* c, int32_t rows, int32_t budget
   kv.page_size = c->page_size;
   kv.max_pages_per_seq = c->max_pages_per_seq > budget ? c->max_pages_per_seq : budget;
   kv.num_pages_total = c->num_pages_total;
-  kv.dtype = S3R_F32;               // partial slots of the grid-split kernel, for both types
+  kv.dtype = dt;
   return plan_attention(kv, rows, budget);
 }
 }  // namespace
@@ -488,7 +489,7 @@ S3R_EXPORT s3r_status s3r_kvq_rollback(const s3r_paged_kvq* kvq, int32_t* contex
 S3R_EXPORT size_t s3r_kvq_attn_workspace_bytes(const s3r_paged_kvq* kvq, s3r_dtype dtype, int32_t rows,
                                                int32_t budget_pages) {
   if (check_kvq_attn(kvq, dtype, rows, budget_pages) != S3R_OK) return 0;
-  return plan_kvq_attention(kvq, rows, budget_pages).ws_bytes;
+  return plan_kvq_attention(kvq, dtype, rows, budget_pages).ws_bytes;
 }
 
 S3R_EXPORT s3r_status s3r_kvq_attn(const s3r_paged_kvq* kvq, const void* q, s3r_dtype dtype, int32_t rows,
@@ -498,7 +499,7 @@ S3R_EXPORT s3r_status s3r_kvq_attn(const s3r_paged_kvq* kvq, const void* q, s3r_
   if (s != S3R_OK) return s;
   if (!q || !out || !aligned16(q) || !aligned16(out) || !std::isfinite(scale)) return S3R_ERR_INVALID_ARG;
   if ((page_list != nullptr) != (budget_pages > 0)) return S3R_ERR_INVALID_ARG;
-  const AttnPlan pl = plan_kvq_attention(kvq, rows, budget_pages);
+  const AttnPlan pl = plan_kvq_attention(kvq, dtype, rows, budget_pages);
   if (!workspace || workspace_bytes < pl.ws_bytes) return S3R_ERR_WORKSPACE;
   KvqAttnParams p;
   std::memset(&p, 0, sizeof(p));
@@ -529,7 +530,7 @@ S3R_EXPORT s3r_status s3r_kvq_attn(const s3r_paged_kvq* kvq, const void* q, s3r_
   p.part_ml = reinterpret_cast<float*>(w + pl.off_ml);
   p.part_o = reinterpret_cast<float*>(w + pl.off_o);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return from_cuda(launch_kvq_attn_f32(*kvq, dtype, p, st));
+  return from_cuda(launch_kvq_attn(*kvq, dtype, p, st));
 }
 
 S3R_EXPORT s3r_status s3r_debug_exp64(const double* x, double* y_tbl, double* y_ref, int32_t n, void* stream) {

@@ -151,25 +151,19 @@ cudaError_t launch_kvq_read(const s3r_paged_kvq& c, const int32_t* start, int32_
 cudaError_t launch_kvq_rollback(const s3r_paged_kvq& c, int32_t* lens, const int32_t* num_accepted, int32_t rows, void* ws,
                                 cudaStream_t st);
 
-struct KvqAttnParams {
-  const void* q;              // [S, R, Hq, D]
-  void* out;
-  float* lse;                 // [S, R, Hq] or null
+// As AttnParams (k_cache, v_cache and the sparse draft's and tree's fields
+// unused), over quantised pages; a launch covers rows r0 .. of the call's R
+// (`rows` = G x the rows of the launch).
+struct KvqAttnParams : AttnParams {
   const uint8_t* pages;       // [num_pages_total, Hkv, page_bytes]
-  const int32_t* block_table;
-  const int32_t* context_lens;
-  const int32_t* page_list;   // [S, Hkv, budget] logical pages (-1: none), or null: every page
-  int32_t S, Hq, Hkv, G, D, P, R;
-  int32_t r0, rows;           // first row of this launch, its packed rows (G x rows of the launch)
-  int32_t max_pages, num_pages_total, budget;
-  int32_t nsplit, chunk_pages;   // f32: grid splits per unit and pages per split
-  float scale_log2;              // scale * log2(e)
-  uint32_t* status;
-  uint32_t* tickets;             // [S * Hkv]
-  float* part_ml;                // [slots, rows, 2]
-  float* part_o;                 // [slots, rows, D]
+  int32_t r0;
 };
-cudaError_t launch_kvq_attn_f32(const s3r_paged_kvq& c, s3r_dtype dt, const KvqAttnParams& p, cudaStream_t st);
+cudaError_t launch_kvq_attn(const s3r_paged_kvq& c, s3r_dtype dt, const KvqAttnParams& p, cudaStream_t st);
+// The tensor-core kernel over a cache of 4 or 8 bits (bf16), and the packed
+// rows one launch of it takes.
+constexpr int kKvqRows4 = 64, kKvqRows8 = 48;
+cudaError_t launch_kvq_attn_tok4(int head_dim, const KvqAttnParams& p, cudaStream_t st);
+cudaError_t launch_kvq_attn_tok8(int head_dim, const KvqAttnParams& p, cudaStream_t st);
 
 struct SamplePlan {
   int32_t nrows;        // rows with statistics (2*gamma+1 per sequence, or num_rows)

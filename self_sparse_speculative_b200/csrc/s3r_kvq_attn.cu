@@ -1,5 +1,6 @@
-// Attention over the quantised paged KV cache on CUDA cores (layout and
-// arithmetic of a held row: s3r_kvq.cuh).
+// Attention over the quantised paged KV cache (layout and arithmetic of a held
+// row: s3r_kvq.cuh): the dispatch, and the float32 kernel on CUDA cores (bf16
+// goes to the tensor-core kernel, s3r_kvq_attn_tok.cuh).
 //
 //   score[i, t] = scale (s_k[t] q_i . n_k[t] + z_k[t] sum q_i)      (= scale q_i . k^_t)
 //   out[i, d]   = sum_t p[i, t] (s_v[t] n_v[t, d] + z_v[t]) / sum_t p[i, t]
@@ -28,12 +29,7 @@ namespace {
 constexpr int kF32Threads = 128;
 constexpr int kF32Tok = 16;
 
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
-template <typename T, int D, int P, int BITS>
+template <int D, int P, int BITS>
 __global__ void __launch_bounds__(kF32Threads) kvq_attn_f32_kernel(const KvqAttnParams p) {
   constexpr KvqLayout Y = kvq_layout(D, P, BITS);
   constexpr int kKStride = D + 4;                        // 16 tokens of one channel on 8 banks apart
@@ -48,7 +44,7 @@ __global__ void __launch_bounds__(kF32Threads) kvq_attn_f32_kernel(const KvqAttn
   if (kvq_bad_context(p, L)) {
     if (split == 0) {
       if (tid == 0) flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
-      kvq_write_empty<T>(p, b, h, tid, kF32Threads);
+      kvq_write_empty<float>(p, b, h, tid, kF32Threads);
     }
     return;
   }
@@ -66,10 +62,10 @@ __global__ void __launch_bounds__(kF32Threads) kvq_attn_f32_kernel(const KvqAttn
   float* sM = sS + rows * kF32Tok;            // [rows]
   float* sL = sM + rows;                      // [rows]
   float* sA = sL + rows;                      // [rows]
-  const T* q = static_cast<const T*>(p.q);
+  const float* q = static_cast<const float*>(p.q);
   for (int idx = tid; idx < rows * D; idx += kF32Threads) {
     const int i = idx / D, d = idx - (idx / D) * D;
-    sQ[idx] = as_float(q[kvq_out_row(p, b, h, i) * D + d]);
+    sQ[idx] = q[kvq_out_row(p, b, h, i) * D + d];
     sO[idx] = 0.f;
   }
   for (int i = tid; i < rows; i += kF32Threads) {
@@ -168,7 +164,7 @@ __global__ void __launch_bounds__(kF32Threads) kvq_attn_f32_kernel(const KvqAttn
     const int i = idx / D, d = idx - (idx / D) * D;
     if (single) {
       const float l = sL[i];
-      put(static_cast<T*>(p.out) + kvq_out_row(p, b, h, i) * D + d, l == 0.f ? 0.f : sO[idx] / l);
+      static_cast<float*>(p.out)[kvq_out_row(p, b, h, i) * D + d] = l == 0.f ? 0.f : sO[idx] / l;
     } else {
       p.part_o[(((size_t)unit * p.nsplit + split) * rows + i) * D + d] = sO[idx];
     }
@@ -190,34 +186,43 @@ __global__ void __launch_bounds__(kF32Threads) kvq_attn_f32_kernel(const KvqAttn
     __syncthreads();
     if (s_ticket == nsplit_u - 1) {
       __threadfence();
-      kvq_combine<T>(p, b, h, unit * p.nsplit, nsplit_u, kF32Threads);
+      kvq_combine<float>(p, b, h, unit * p.nsplit, nsplit_u, kF32Threads);
       if (tid == 0) p.tickets[unit] = 0u;
     }
   }
 }
 
-template <typename T, int D, int P, int BITS>
+template <int D, int P, int BITS>
 cudaError_t launch_f32(const KvqAttnParams& p, cudaStream_t st) {
   const size_t smem = sizeof(float) * ((size_t)2 * p.rows * D + kF32Tok * (2 * D + 4) + (size_t)p.rows * kF32Tok + 3 * p.rows);
-  cudaError_t e = cudaFuncSetAttribute(kvq_attn_f32_kernel<T, D, P, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(kvq_attn_f32_kernel<D, P, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kvq_attn_f32_kernel<T, D, P, BITS>, dim3(p.nsplit, p.Hkv, p.S), dim3(kF32Threads), smem, st, 1, p);
-}
-template <int D, int P, int BITS>
-cudaError_t launch_type(s3r_dtype dt, const KvqAttnParams& p, cudaStream_t st) {
-  return dt == S3R_F32 ? launch_f32<float, D, P, BITS>(p, st) : launch_f32<__nv_bfloat16, D, P, BITS>(p, st);
+  return launch_kernel(kvq_attn_f32_kernel<D, P, BITS>, dim3(p.nsplit, p.Hkv, p.S), dim3(kF32Threads), smem, st, 1, p);
 }
 template <int D, int P>
-cudaError_t launch_f32_bits(s3r_dtype dt, int bits, const KvqAttnParams& p, cudaStream_t st) {
-  return bits == 4 ? launch_type<D, P, 4>(dt, p, st) : launch_type<D, P, 8>(dt, p, st);
+cudaError_t launch_f32_bits(int bits, const KvqAttnParams& p, cudaStream_t st) {
+  return bits == 4 ? launch_f32<D, P, 4>(p, st) : launch_f32<D, P, 8>(p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_kvq_attn_f32(const s3r_paged_kvq& c, s3r_dtype dt, const KvqAttnParams& p, cudaStream_t st) {
-  if (c.head_dim == 64)
-    return c.page_size == 16 ? launch_f32_bits<64, 16>(dt, c.bits, p, st) : launch_f32_bits<64, 64>(dt, c.bits, p, st);
-  return c.page_size == 16 ? launch_f32_bits<128, 16>(dt, c.bits, p, st) : launch_f32_bits<128, 64>(dt, c.bits, p, st);
+cudaError_t launch_kvq_attn(const s3r_paged_kvq& c, s3r_dtype dt, const KvqAttnParams& p, cudaStream_t st) {
+  if (dt == S3R_F32) {
+    if (c.head_dim == 64)
+      return c.page_size == 16 ? launch_f32_bits<64, 16>(c.bits, p, st) : launch_f32_bits<64, 64>(c.bits, p, st);
+    return c.page_size == 16 ? launch_f32_bits<128, 16>(c.bits, p, st) : launch_f32_bits<128, 64>(c.bits, p, st);
+  }
+  // more packed rows than one launch takes: equal shares of the rows, one launch each
+  const int most = (c.bits == 4 ? kKvqRows4 : kKvqRows8) / p.G;
+  const int launches = (p.R + most - 1) / most, per = (p.R + launches - 1) / launches;
+  for (int r0 = 0; r0 < p.R; r0 += per) {
+    KvqAttnParams q = p;
+    q.r0 = r0;
+    q.rows = p.G * (p.R - r0 < per ? p.R - r0 : per);
+    const cudaError_t e = c.bits == 4 ? launch_kvq_attn_tok4(c.head_dim, q, st) : launch_kvq_attn_tok8(c.head_dim, q, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace s3r

@@ -3,17 +3,18 @@ single rows and verification rows, every head layout, lengths from one token,
 odd sizes, page lists, rows that see nothing, NaN in masked places, captured
 and repeated calls, caches past 32-bit offsets.
 
-Error bound of an output (u = 2^-24, A = sum p |v| / sum p, B = sum p s_v / sum p,
-N = the largest whole number met: 31 at 4 bits and 543 at 8 bits, offsets
-included; T tokens):
+Error bound of an output (u = 2^-24, A = sum p |v| / sum p, B = sum p s_v / sum p, n at most
+N = 2^bits - 1, c = N / 2, T tokens):
 - a score's products are exact in float32 and are summed with at most T_k = 32 +
-  D / 4 roundings of partial sums no larger than scale s_k N sum |q| (+ scale |z_k| sum |q|),
-  so it is off by at most e = T_k u scale (s_k N + |z_k|) sum |q|; with the
-  base-2 exponential's 2^-21 relative error a weight is off by e + 2^-21 + 4 u |score|
-  of itself, which moves the output by at most twice that times A;
-- bf16: a weight p s_v is rounded to bf16 (2^-8 of itself at most half a step: 2^-8 A)
-  and so is the output (2^-8 |out|);
-- sums over T tokens: at most T + 64 roundings of partial sums no larger than N B + A.
+  D / 4 roundings of partial sums no larger than scale (s_k (N + 1) + |z_k|) sum |q|, so it is off by
+  at most e = T_k u scale (s_k (N + 1) + |z_k|) sum |q|. bf16: a query is two e4m3 terms of q 2^k, exact
+  but for values so small that they round to the terms' spacing of 2^-14, where the row's largest is at least 128 (4
+  bits) or 8 (8 bits): each of D values off by at most 2^-15 / 128 or 2^-15 / 8 of the row's largest, times scale s_k N.
+  With the base-2 exponential's 2^-21 relative error a weight is off by e + 2^-21 +
+  4 u |score| of itself, which moves the output by at most twice that times A;
+- bf16: a weight w = p s_v is two e4m3 terms: off by at most 2^-9 w + 2^-15, where the row's largest weight is at least 64;
+  the error meets n - c, at most c in size: c (2^-9 B + T 2^-21 max s_v); the output's rounding is 2^-8 |out|;
+- sums over T tokens: at most T + 64 roundings of partial sums no larger than 2 (N + 1) B + A.
 The log-sum-exp is off by at most max e + 2^-21 + (T + 64) u + 4 u |lse|."""
 import numpy as np
 import pytest
@@ -73,7 +74,7 @@ class Case:
 
     def check(self, seqs=None, skip=()):
         pages, lists = self.pages.cpu().numpy(), None if self.list is None else self.list.cpu().numpy()
-        N = 31 if self.bits == 4 else 543
+        N = 2 ** self.bits - 1
         for b in range(self.S) if seqs is None else seqs:
             if b in skip:
                 continue
@@ -87,13 +88,17 @@ class Case:
             ref, lse, A, B = Q.attend(q, held, self.scale, self.rows, pos)
             T = L if pos is None else max(len(x) for x in pos)
             sumq = np.abs(q.astype(np.float64)).sum(-1)                         # [R, Hq]
-            span = (held["sk"] * N + np.abs(held["zk"])).max(0).repeat(self.G)  # [Hq]
+            span = (held["sk"] * (N + 1) + np.abs(held["zk"])).max(0).repeat(self.G)   # [Hq]
             e = (32 + self.D / 4) * U * self.scale * span * sumq
+            if self.dtype == "bf16":
+                e = e + (self.D * 2.0 ** -15 / (128 if self.bits == 4 else 8) * np.abs(q).max(-1).astype(np.float64)
+                         * self.scale * N * held["sk"].max(0).repeat(self.G))
             top = np.where(np.isfinite(lse), np.abs(lse), 0.0)
             w = e + 2.0 ** -21 + 4 * U * (top + np.log(max(T, 1)) + 1)
-            tol = 2 * w[..., None] * A + (T + 64) * U * (N * B[..., None] + A) + 1e-30
+            tol = 2 * w[..., None] * A + (T + 64) * U * (2 * (N + 1) * B[..., None] + A) + 1e-30
             if self.dtype == "bf16":
-                tol = tol + 2.0 ** -8 * A * 1.01 + 2.0 ** -8 * np.abs(ref) * 1.01
+                few = T * 2.0 ** -21 * held["sv"].max(0).repeat(self.G)[None, :, None]
+                tol = tol + 1.01 * (N / 2 * (2.0 ** -9 * B[..., None] + few) + 2.0 ** -8 * np.abs(ref))
             out, got = self.out[b].double().cpu().numpy(), self.lse[b].double().cpu().numpy()
             bad = np.abs(out - ref) > tol
             assert not bad.any(), (b, np.argwhere(bad)[:3], out[bad][:3], ref[bad][:3], tol[bad][:3])
@@ -385,9 +390,10 @@ def test_a_run_of_the_calls_together(bits):
         s3r.s3r_kvq_attn(kvq, q, "bf16", rows, 0.09, out, lse, wa[rows])
         for b in range(S):
             held = Q.held_rows(host, table[b], hl[b], D, P, bits)
-            ref, rl, A, _ = Q.attend(q[b].float().cpu().numpy(), held, 0.09, rows)
-            # two bf16 roundings of at most half a step each, and float32 sums (2^-10 of A is far above them)
-            tol = 2.0 ** -8 * (A + np.abs(ref)) * 1.01 + 2.0 ** -10 * A
+            ref, rl, A, B = Q.attend(q[b].float().cpu().numpy(), held, 0.09, rows)
+            # the weights' and the output's roundings as above; scores and float32 sums are far below 2^-9 of A
+            few = hl[b] * 2.0 ** -21 * held["sv"].max()
+            tol = 1.01 * ((2 ** bits - 1) / 2 * (2.0 ** -9 * B[..., None] + few) + 2.0 ** -8 * np.abs(ref)) + 2.0 ** -9 * A
             assert (np.abs(out[b].double().cpu().numpy() - ref) <= tol).all()
             assert np.abs(lse[b].double().cpu().numpy() - rl).max() < 1e-3
 
