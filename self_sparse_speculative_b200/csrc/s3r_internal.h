@@ -161,7 +161,7 @@ struct KvqAttnParams : AttnParams {
 cudaError_t launch_kvq_attn(const s3r_paged_kvq& c, s3r_dtype dt, const KvqAttnParams& p, cudaStream_t st);
 // The tensor-core kernel over a cache of 4 or 8 bits (bf16), and the packed
 // rows one launch of it takes.
-constexpr int kKvqRows4 = 64, kKvqRows8 = 48;
+constexpr int kKvqRows = 64;
 cudaError_t launch_kvq_attn_tok4(int head_dim, const KvqAttnParams& p, cudaStream_t st);
 cudaError_t launch_kvq_attn_tok8(int head_dim, const KvqAttnParams& p, cudaStream_t st);
 

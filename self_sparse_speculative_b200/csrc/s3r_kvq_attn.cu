@@ -213,7 +213,7 @@ cudaError_t launch_kvq_attn(const s3r_paged_kvq& c, s3r_dtype dt, const KvqAttnP
     return c.page_size == 16 ? launch_f32_bits<128, 16>(c.bits, p, st) : launch_f32_bits<128, 64>(c.bits, p, st);
   }
   // more packed rows than one launch takes: equal shares of the rows, one launch each
-  const int most = (c.bits == 4 ? kKvqRows4 : kKvqRows8) / p.G;
+  const int most = kKvqRows / p.G;
   const int launches = (p.R + most - 1) / most, per = (p.R + launches - 1) / launches;
   for (int r0 = 0; r0 < p.R; r0 += per) {
     KvqAttnParams q = p;

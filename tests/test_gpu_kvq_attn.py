@@ -7,13 +7,14 @@ Error bound of an output (u = 2^-24, A = sum p |v| / sum p, B = sum p s_v / sum 
 N = 2^bits - 1, c = N / 2, T tokens):
 - a score's products are exact in float32 and are summed with at most T_k = 32 +
   D / 4 roundings of partial sums no larger than scale (s_k (N + 1) + |z_k|) sum |q|, so it is off by
-  at most e = T_k u scale (s_k (N + 1) + |z_k|) sum |q|. bf16: a query is two e4m3 terms of q 2^k, exact
-  but for values so small that they round to the terms' spacing of 2^-14, where the row's largest is at least 128 (4
-  bits) or 8 (8 bits): each of D values off by at most 2^-15 / 128 or 2^-15 / 8 of the row's largest, times scale s_k N.
+  at most e = T_k u scale (s_k (N + 1) + |z_k|) sum |q|. bf16: a query is met as float16 of q 2^k, exact
+  but for values so small that they round to its spacing of 2^-24, where the row's largest is at least 128:
+  each of D values off by at most 2^-32 of the row's largest, times scale s_k N.
   With the base-2 exponential's 2^-21 relative error a weight is off by e + 2^-21 +
   4 u |score| of itself, which moves the output by at most twice that times A;
-- bf16: a weight w = p s_v is two e4m3 terms: off by at most 2^-9 w + 2^-15, where the row's largest weight is at least 64;
-  the error meets n - c, at most c in size: c (2^-9 B + T 2^-21 max s_v); the output's rounding is 2^-8 |out|;
+- bf16: a weight w = p s_v is rounded to float16: off by at most 2^-12 w + 2^-25, where the row's largest weight is at
+  least 2^8; the error meets n - c, at most c + 1 in size: (c + 1) (2^-12 B + T 2^-33 max s_v); the output's rounding
+  is 2^-8 |out|;
 - sums over T tokens: at most T + 64 roundings of partial sums no larger than 2 (N + 1) B + A.
 The log-sum-exp is off by at most max e + 2^-21 + (T + 64) u + 4 u |lse|."""
 import numpy as np
@@ -91,14 +92,13 @@ class Case:
             span = (held["sk"] * (N + 1) + np.abs(held["zk"])).max(0).repeat(self.G)   # [Hq]
             e = (32 + self.D / 4) * U * self.scale * span * sumq
             if self.dtype == "bf16":
-                e = e + (self.D * 2.0 ** -15 / (128 if self.bits == 4 else 8) * np.abs(q).max(-1).astype(np.float64)
-                         * self.scale * N * held["sk"].max(0).repeat(self.G))
+                e = e + self.D * 2.0 ** -32 * np.abs(q).max(-1) * self.scale * N * held["sk"].max(0).repeat(self.G)
             top = np.where(np.isfinite(lse), np.abs(lse), 0.0)
             w = e + 2.0 ** -21 + 4 * U * (top + np.log(max(T, 1)) + 1)
             tol = 2 * w[..., None] * A + (T + 64) * U * (2 * (N + 1) * B[..., None] + A) + 1e-30
             if self.dtype == "bf16":
-                few = T * 2.0 ** -21 * held["sv"].max(0).repeat(self.G)[None, :, None]
-                tol = tol + 1.01 * (N / 2 * (2.0 ** -9 * B[..., None] + few) + 2.0 ** -8 * np.abs(ref))
+                few = T * 2.0 ** -33 * held["sv"].max(0).repeat(self.G)[None, :, None]
+                tol = tol + 1.01 * ((N / 2 + 1) * (2.0 ** -12 * B[..., None] + few) + 2.0 ** -8 * np.abs(ref))
             out, got = self.out[b].double().cpu().numpy(), self.lse[b].double().cpu().numpy()
             bad = np.abs(out - ref) > tol
             assert not bad.any(), (b, np.argwhere(bad)[:3], out[bad][:3], ref[bad][:3], tol[bad][:3])
@@ -391,9 +391,8 @@ def test_a_run_of_the_calls_together(bits):
         for b in range(S):
             held = Q.held_rows(host, table[b], hl[b], D, P, bits)
             ref, rl, A, B = Q.attend(q[b].float().cpu().numpy(), held, 0.09, rows)
-            # the weights' and the output's roundings as above; scores and float32 sums are far below 2^-9 of A
-            few = hl[b] * 2.0 ** -21 * held["sv"].max()
-            tol = 1.01 * ((2 ** bits - 1) / 2 * (2.0 ** -9 * B[..., None] + few) + 2.0 ** -8 * np.abs(ref)) + 2.0 ** -9 * A
+            # the weights' and the output's roundings as above; scores and float32 sums are far below 2^-10 of A
+            tol = 1.01 * (2 ** (bits - 1) * 2.0 ** -12 * B[..., None] + 2.0 ** -8 * np.abs(ref)) + 2.0 ** -10 * A
             assert (np.abs(out[b].double().cpu().numpy() - ref) <= tol).all()
             assert np.abs(lse[b].double().cpu().numpy() - rl).max() < 1e-3
 
