@@ -33,12 +33,11 @@
 //
 // Warps: two softmax warpgroups (thread = token), two unpacking ones (keys,
 // values), one producer (a bulk copy per (page, head) into an NS-stage ring of
-// 128 tokens), one MMA issuer that polls its barriers and issues whichever
-// product is ready. A stage's softmax is a chain of waits and latencies of
-// about 1500 cycles, twice what a stage's bytes take, so up to 16 rows the
-// warpgroups take alternate stages (ALT): each keeps its own references, sums
-// and O^T, merged at the end of a segment. With more rows the arithmetic
-// counts and the warpgroups share the rows of every stage. Work is split over
+// 128 tokens), one MMA issuer per product. A stage's softmax is a chain of
+// waits and latencies of about 1500 cycles, twice what a stage's bytes take, so
+// up to 24 rows the warpgroups take alternate stages (ALT): each keeps its own
+// references, sums and O^T, merged at the end of a segment. More rows do not
+// fit a thread's registers: there the warpgroups share the rows of every stage. Work is split over
 // CTAs as in the bf16 attention (s3r_attn_sched.cuh), units shared by several
 // CTAs merge by log-sum-exp in the last one to finish.
 #pragma once
@@ -59,23 +58,25 @@ namespace s3r {
 namespace kvq {
 
 constexpr int kTok = 128;                    // tokens per stage
-constexpr float kTop = 8.0f;                 // log2 of the largest weight when a row's reference is raised
-constexpr float kTau = 7.0f;                 // lazy reference slack, log2 units: weights stay below 2^15
 constexpr float kNuInit = 1e30f;             // -(reference) before the first score of a segment
 constexpr int kSmemBudget = 232448 - 10240;  // beside the static arrays
 constexpr int kMaxPend = 8;                  // deferred merges of units per CTA
-constexpr int kThreads = 576;                // 8 softmax and 8 unpacking warps, producer, MMA issuer
+constexpr int kThreads = 608;                // 8 softmax and 8 unpacking warps, producer, two MMA issuers
 constexpr int kSoft = 256;                   // softmax threads
-constexpr int kProducer = 16, kMma = 17;
+constexpr int kProducer = 16, kMmaQk = 17, kMmaPv = 18;
 
-// ALT: NR rows, both warpgroups; else 2 NR rows, NR each.
+// ALT: NR rows, both warpgroups; else 2 NR rows, NR each. E4: e4m3 operands,
+// two terms of a row in columns NRT apart.
 template <int NR, bool ALT, int D, int BITS>
 struct Lay {
+  static constexpr bool E4 = BITS == 4 && ALT;
   static constexpr int NRT = ALT ? NR : 2 * NR;
-  static constexpr int N = (NRT + 15) / 16 * 16;
-  static constexpr int kKCols = D / 2;                     // TMEM columns of a stage's keys
-  static constexpr uint32_t kQBytes = N * D * 2;           // [64 k][N rows][128 B], two (segment parity)
-  static constexpr uint32_t kPBytes = N * kTok * 2;        // two (stage parity)
+  static constexpr int N = ((E4 ? 2 * NRT : NRT) + 15) / 16 * 16;
+  static constexpr int kTile = E4 ? 32 : 64;               // TMEM columns of 128 numbers a lane
+  static constexpr int kKCols = kTile * D / 128;           // of a stage's keys
+  static constexpr uint32_t kRowK = E4 ? 128 : 64;         // of k in one 128-byte row of Q and w
+  static constexpr uint32_t kQBytes = N * 128 * ((D + kRowK - 1) / kRowK);   // [blocks of kRowK][N rows][128 B], two (segment parity)
+  static constexpr uint32_t kPBytes = N * 128 * (kTok / kRowK);              // two (stage parity)
   static constexpr uint32_t kXBytes = ALT ? NR * 128 * 4 : 0;   // O^T of the second warpgroup, [row][channel]
   static constexpr uint32_t kStage = 2 * (kTok * D * BITS / 8) + 8 * kTok;
   static constexpr uint32_t kOffP = 2 * kQBytes;
@@ -86,20 +87,27 @@ struct Lay {
   static constexpr uint32_t kDynBytes = kOffKV + kNS * kStage + 1024;
   // TMEM columns: NB key tiles, NB value tiles, S^T[2], O^T[1 or 2]
   static constexpr int kAcc = ALT ? 4 : 3;
-  static constexpr int NB = kAcc * N + 384 <= 512 ? 3 : 2;
-  static constexpr uint32_t kColK = 0, kColV = 64 * NB, kColS = 128 * NB, kColO = 128 * NB + 2 * N;
-  static_assert(kNS >= 2, "the ring needs two stages");
-  static_assert(128 * NB + kAcc * N <= 512, "TMEM columns");
+  static constexpr int kNBraw = (512 - kAcc * N) / (2 * kTile);
+  static constexpr int NB = kNBraw > 4 ? 4 : kNBraw;
+  static constexpr uint32_t kColK = 0, kColV = kTile * NB, kColS = 2 * kTile * NB, kColO = kColS + 2 * N;
+  // log2 of the largest weight when a row's reference is raised, and the
+  // slack before it is raised again: weights stay below 256 or 2^15
+  static constexpr float kTop = E4 ? 6.f : 8.f, kTau = E4 ? 2.f : 7.f;
+  static_assert(kNS >= 2 && NB >= 2, "the rings need two stages");
+  static_assert(2 * kTile * NB + kAcc * N <= 512, "TMEM columns");
 };
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16 (f16 inputs, f32 accumulate), 16 of k.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+// D[tmem] (+)= A[tmem] * B[smem]^T, f32 accumulate: 32 of k of e4m3 or 16 of f16.
+template <bool E4>
+__device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (E4)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 // 4 columns of this warp's lanes.
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, float* v) {
@@ -114,8 +122,8 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const float* v) {
                :: "r"(taddr), "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
                   "r"(__float_as_uint(v[3])));
 }
-// Registers from the unpacking warpgroups to the softmax ones: with 576
-// threads launched at 96 registers, 256 x 128 + 256 x 64 + 64 x 96 is the same total.
+// Registers from the unpacking warpgroups to the softmax ones: with 608
+// threads launched at 96 registers, 256 x 128 + 256 x 64 + 96 x 96 is the same total.
 constexpr int kLaunchRegs = 96;
 template <bool SOFTMAX>
 __device__ __forceinline__ void split_registers() {
@@ -127,6 +135,15 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
+}
+// 16 registers to this warp's TMEM lanes, 16 consecutive columns.
+__device__ __forceinline__ void tmem_st16_raw(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 // 32 registers to this warp's TMEM lanes, 32 consecutive columns.
 __device__ __forceinline__ void tmem_st32_raw(uint32_t taddr, const uint32_t* r) {
@@ -147,8 +164,8 @@ __device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void* src, ui
                :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy) : "memory");
 }
 
-// Instruction descriptor, kind::f16 with f16 A/B and f32 accumulator, both K-major.
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+// Instruction descriptor, f16 A/B (kind::f16) or e4m3 A/B (kind::f8f6f4), f32 accumulator, both K-major.
+__host__ __device__ constexpr uint32_t idesc_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
@@ -173,10 +190,44 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t* r) {
   }
 }
 
+// The eight 4-bit numbers of a word as e4m3 (n 2^-9): the even ones, the odd
+// ones. ALT: 15 - n for the odd ones (every other token of the values).
+template <bool ALT>
+__device__ __forceinline__ void unpack_e4(uint32_t w, uint32_t* r) {
+  r[0] = w & 0x0f0f0f0fu;
+  r[1] = ((w >> 4) ^ (ALT ? ~0u : 0u)) & 0x0f0f0f0fu;
+}
+
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_of(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+// Two float16 values as e4m3 terms hi + kLo lo. A value of 9 significant bits
+// is exact (hi: 4 bits, rounded to nearest; what is left: 16 steps at most)
+// down to the spacing of lo, 2^-14.
+constexpr float kLo = 1.f / 32;
+struct Split { uint32_t hi, lo; };
+__device__ __forceinline__ Split split2(uint32_t h2) {
+  Split s;
+  s.hi = e4m3x2_of(h2);
+  uint32_t hf;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hf) : "h"((uint16_t)s.hi));
+  const __half2 k = __float2half2_rn(32.f), m = __float2half2_rn(-32.f);
+  const __half2 lo = __hfma2(*reinterpret_cast<const __half2*>(&hf), m, __hmul2(*reinterpret_cast<const __half2*>(&h2), k));
+  s.lo = e4m3x2_of(*reinterpret_cast<const uint32_t*>(&lo));
+  return s;
+}
+// x rounded to 9 significant bits.
+__device__ __forceinline__ float round9(float x) {
+  const float c = x * 32769.f;
+  return __fsub_rn(c, __fsub_rn(c, x));
 }
 
 // Reduce C per-row values over the warp: lane l ends with row l % C.
@@ -219,22 +270,13 @@ __device__ __forceinline__ void warp_part(float* v, float (*red)[32], int q4, in
   }
 }
 
-// Barrier over a softmax warpgroup (ALT, barriers 1 and 2) or both (barrier 1).
-template <bool ALT>
-__device__ __forceinline__ void sync_softmax(int wg) {
-  if constexpr (ALT) asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-  else asm volatile("bar.sync 1, 256;" ::: "memory");
-}
+// Barrier over a softmax warpgroup (barriers 1 and 2).
+__device__ __forceinline__ void sync_wg(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
 // Number of its threads whose predicate is true.
-template <bool ALT>
-__device__ __forceinline__ int count_softmax(int wg, bool pred) {
+__device__ __forceinline__ int count_wg(int wg, bool pred) {
   int r;
-  if constexpr (ALT)
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.popc.u32 %0, %2, 128, p;\n\t}"
-                 : "=r"(r) : "r"((int)pred), "r"(1 + wg) : "memory");
-  else
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.popc.u32 %0, 1, 256, p;\n\t}"
-                 : "=r"(r) : "r"((int)pred) : "memory");
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.popc.u32 %0, %2, 128, p;\n\t}"
+               : "=r"(r) : "r"((int)pred), "r"(1 + wg) : "memory");
   return r;
 }
 
@@ -248,9 +290,12 @@ template <int NR, bool ALT, int D, int P, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p) {
   using L = Lay<NR, ALT, D, BITS>;
   constexpr KvqLayout Y = kvq_layout(D, P, BITS);
+  constexpr int kUnit = Y.unit;                          // bytes of a V piece
   constexpr int NRT = L::NRT, N = L::N, NB = L::NB, NS = L::kNS;
   constexpr int ppt = kTok / P;                          // pages per stage
-  constexpr float kMid = BITS == 4 ? 8.f : 128.f;
+  constexpr bool E4 = L::E4;
+  constexpr float kTop = L::kTop, kTau = L::kTau;
+  constexpr float kMid = E4 ? 0.f : BITS == 4 ? 8.f : 128.f;   // subtracted from the numbers
   static_assert(ppt * Y.page_bytes == (int)L::kStage, "stage bytes");
   extern __shared__ __align__(1024) uint8_t dyn_raw[];
   uint8_t* dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
@@ -333,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   uint8_t* sKV = dyn + L::kOffKV;
   const uint32_t aQ = smem_addr(sQ), aP = smem_addr(sP), aKV = smem_addr(sKV);
 
-  if (warp == kMma) {
+  if (warp == kMmaQk) {
     tmem_alloc(smem_addr(&s_tmem), 512);
     tmem_relinquish();
   }
@@ -350,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     }
     for (int i = 0; i < 2; ++i) mbar_init(BAR(B_PF + i), ALT ? 4 : 8);
     mbar_init(BAR(B_QF), 8);
-    mbar_init(BAR(B_TD), 1);
+    mbar_init(BAR(B_TD), 2);
     mbar_init(BAR(B_X), 4);
     mbar_init(BAR(B_Y), 4);
     s_abort = 0;
@@ -434,88 +479,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     // drain: wait until every issued copy has landed
     if (lane == 0)
       for (int k = max(0, g - NS); k < g; ++k) mbar_wait_drain(BAR(B_FULL + k % NS), (k / NS) & 1, p.status);
-  } else if (warp == kMma) {
-    // ======================================================= MMA issuer
-    // The whole warp runs the loop on values made uniform by shuffles and one
-    // elected lane issues: an MMA then costs 10 cycles to issue instead of 46
-    // from a lane's own branch (N = 16, measured), and a commit about 80 -
-    // there is one per tile, which both the unpacking warps (tile free) and
-    // the softmax (product done) wait on.
-    constexpr uint32_t idesc = idesc_f16_f32(128, N);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    Cursor qc = cursor_begin(p, s_prefix, lo, hi, W, ppt);
-    Cursor pc = qc;
-    // Q and w: K-major, 128-byte rows, 8-row groups 1024 B apart; a K16
-    // step is 32 bytes inside the swizzle row, the next 64 of k N x 128 B
-    // further. A tile's K16 step is 8 TMEM columns.
-    const uint64_t dQ0 = smem_desc_sw128(aQ, 16, 1024), dP0 = smem_desc_sw128(aP, 16, 1024);
-    constexpr uint32_t kBlock = (N * 128) >> 4;
+  } else if (warp >= kMmaQk) {
+    // ======================================================= MMA issuers
+    // One warp for each product, in stage order. The whole warp runs the loop
+    // on values made uniform by shuffles and one elected lane issues: an MMA
+    // then costs 10 cycles to issue instead of 46 from a lane's own branch
+    // (N = 16, measured), and a commit about 80 - there is one per tile, which
+    // both the unpacking warps (tile free) and the softmax (product done) wait on.
+    // QK(g) needs its keys, w(g - 2) written (S^T buffer g & 1 has been read)
+    // and first in a segment the segment's Q; PV(g) needs w(g) and its values.
+    constexpr uint32_t idesc = idesc_f32(128, N);
     auto uni = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
-    auto ready = [&](int bar, uint32_t parity) { return uni(mbar_test_wait(BAR(bar), parity)) != 0u; };
-    // QK(g) needs its keys (first in a segment, also the segment's Q) and
-    // PV(g - 2) issued (w(g - 2) written: S^T buffer g & 1 has been read);
-    // PV(g) needs w(g) and its values. Each tile is issued as soon as it is
-    // ready. Bounded: no progress for the wait limit flags a timeout and stops.
-    auto issue_qk = [&]() {
-      tc_fence_after();
-      const uint32_t dS = uni(tm + L::kColS + (qc.g & 1) * N), a = uni(tm + L::kColK + qc.g % NB * 64);
-      const uint32_t bar = uni(BAR(B_KE + qc.g % NB)), step = uni((qc.s & 1) * (L::kQBytes >> 4));
-      if (elect_one()) {
+    const uint32_t tm = uni(tmem);
+    // Q and w: K-major, 128-byte rows, 8-row groups 1024 B apart; a step of
+    // k is 32 bytes inside the swizzle row, the next row N x 128 B further.
+    // A tile's step is 8 TMEM columns.
+    const uint64_t dB0 = smem_desc_sw128(warp == kMmaQk ? aQ : aP, 16, 1024);
+    constexpr uint32_t kBlock = (N * 128) >> 4;
+    for (Cursor c = cursor_begin(p, s_prefix, lo, hi, W, ppt); uni(c.valid); cursor_next(p, s_prefix, hi, W, ppt, c)) {
+      const int buf = c.g % NB;
+      if (warp == kMmaQk) {
+        bool ok = mbar_wait(BAR(B_KF + buf), (c.g / NB) & 1, &s_abort, p.status);
+        if (c.g >= 2) ok = ok && mbar_wait(BAR(B_PF + (c.g & 1)), ((c.g >> 1) & 1) ^ 1, &s_abort, p.status);
+        if (c.j == 0) ok = ok && mbar_wait(BAR(B_QF), c.s & 1, &s_abort, p.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint32_t d = uni(tm + L::kColS + (c.g & 1) * N), a = uni(tm + L::kColK + buf * L::kTile);
+        const uint32_t bar = uni(BAR(B_KE + buf)), step = uni((c.s & 1) * (L::kQBytes >> 4));
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_f16_ta(dS, a + kk * 8, dQ0 + step + (kk >> 2) * kBlock + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
-        umma_commit(bar);
-      }
-      __syncwarp();
-      cursor_next(p, s_prefix, hi, W, ppt, qc);
-    };
-    auto issue_pv = [&]() {
-      tc_fence_after();
-      const uint32_t dO = uni(tm + L::kColO + (ALT ? (pc.g & 1) * N : 0)), a = uni(tm + L::kColV + pc.g % NB * 64);
-      const uint32_t first = uni(pc.j >= (ALT ? 2 : 1) ? 1u : 0u), bar = uni(BAR(B_VE + pc.g % NB));
-      const uint32_t step = uni((pc.g & 1) * (L::kPBytes >> 4));
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < kTok / 16; ++kk)
-          umma_f16_ta(dO, a + kk * 8, dP0 + step + (kk >> 2) * kBlock + (kk & 3) * 2, idesc, kk > 0 ? 1u : first);
-        umma_commit(bar);
-      }
-      __syncwarp();
-      cursor_next(p, s_prefix, hi, W, ppt, pc);
-    };
-    unsigned long long idle_since = 0;
-    uint32_t spins = 0;
-    while (uni(pc.valid)) {
-      bool progress = false;
-      if (ready(B_PF + (pc.g & 1), (pc.g >> 1) & 1) && ready(B_VF + pc.g % NB, (pc.g / NB) & 1)) {
-        issue_pv();
-        progress = true;
-      }
-      if (uni(qc.valid && qc.g <= pc.g + 1) && (qc.j != 0 || ready(B_QF, qc.s & 1)) &&
-          ready(B_KF + qc.g % NB, (qc.g / NB) & 1)) {
-        issue_qk();
-        progress = true;
-      }
-      if (progress) {
-        idle_since = 0;
-        continue;
-      }
-      if ((++spins & 63u) == 0) {
-        bool stop = false;
-        if (lane == 0) {
-          const unsigned long long now = globaltimer_ns();
-          if (*(volatile int*)&s_abort) {
-            stop = true;
-          } else if (idle_since == 0) {
-            idle_since = now;
-          } else if (now - idle_since > kWaitLimitNs) {
-            *(volatile int*)&s_abort = 1;
-            flag_status(p.status, S3R_DEV_WAIT_TIMEOUT);
-            stop = true;
-          }
+          for (int kk = 0; kk < L::kKCols / 8; ++kk)
+            umma_ta<E4>(d, a + kk * 8, dB0 + step + (kk >> 2) * kBlock + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
+          umma_commit(bar);
         }
-        if (uni(stop)) break;
+      } else {
+        bool ok = mbar_wait(BAR(B_VF + buf), (c.g / NB) & 1, &s_abort, p.status);
+        ok = ok && mbar_wait(BAR(B_PF + (c.g & 1)), (c.g >> 1) & 1, &s_abort, p.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint32_t d = uni(tm + L::kColO + (ALT ? (c.g & 1) * N : 0)), a = uni(tm + L::kColV + buf * L::kTile);
+        const uint32_t first = uni(c.j >= (ALT ? 2 : 1) ? 1u : 0u), bar = uni(BAR(B_VE + buf));
+        const uint32_t step = uni((c.g & 1) * (L::kPBytes >> 4));
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < L::kTile / 8; ++kk)
+            umma_ta<E4>(d, a + kk * 8, dB0 + step + (kk >> 2) * kBlock + (kk & 3) * 2, idesc, kk > 0 ? 1u : first);
+          umma_commit(bar);
+        }
       }
+      __syncwarp();
     }
     if (elect_one()) umma_commit(BAR(B_TD));
     __syncwarp();
@@ -534,48 +546,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint8_t* stage = sKV + st * L::kStage;
-      // 64 columns (32 for keys of 64 channels) in halves of 32
-      auto put = [&](int col, const uint32_t* r) {
-        tmem_st32_raw(tmem + lane_base + (keys ? L::kColK : L::kColV) + buf * 64 + col, r);
+      const uint32_t dst = tmem + lane_base + (keys ? L::kColK : L::kColV) + buf * L::kTile;
+      const uint8_t* row = stage + (t / P) * Y.page_bytes + (t % P) * 16;
+      constexpr int kWordsPage = P * BITS / 32;          // words of a channel in one page: 2, 4, 8 or 16
+      // words k .. k + 3 of this token's channels / of this channel's tokens
+      auto key_words = [&](int k) { return *reinterpret_cast<const uint4*>(row + (k / 4) * (P * 16)); };
+      auto value_words = [&](int k) {
+        const int pg = k / kWordsPage;
+        if constexpr (kUnit == 16)
+          return *reinterpret_cast<const uint4*>(stage + pg * Y.page_bytes + Y.off_v + (k % kWordsPage / 4 * D + t) * 16);
+        const uint2 v0 = *reinterpret_cast<const uint2*>(stage + pg * Y.page_bytes + Y.off_v + t * 8);   // two pages of two words
+        const uint2 v1 = *reinterpret_cast<const uint2*>(stage + (pg + 1) * Y.page_bytes + Y.off_v + t * 8);
+        return make_uint4(v0.x, v0.y, v1.x, v1.y);
       };
-      constexpr int kHalfWords = 64 * BITS / 32;         // words of 32 columns' numbers: 8 or 16
-      if (keys) {
-        const uint8_t* row = stage + (t / P) * Y.page_bytes + (t % P) * 16;
+      if constexpr (E4) {
+        uint32_t r[32];
+        if (keys) {
 #pragma unroll
-        for (int half = 0; half < L::kKCols / 32; ++half) {
-          uint32_t r[32];
-#pragma unroll
-          for (int k = 0; k < kHalfWords; k += 4) {
-            const uint4 w = *reinterpret_cast<const uint4*>(row + ((half * kHalfWords + k) / 4) * (P * 16));
-            unpack<BITS>(w.x, r + k * 16 / BITS);
-            unpack<BITS>(w.y, r + (k + 1) * 16 / BITS);
-            unpack<BITS>(w.z, r + (k + 2) * 16 / BITS);
-            unpack<BITS>(w.w, r + (k + 3) * 16 / BITS);
+          for (int k = 0; k < L::kKCols / 2; k += 4) {
+            const uint4 w = key_words(k);
+            unpack_e4<false>(w.x, r + 2 * k);
+            unpack_e4<false>(w.y, r + 2 * k + 2);
+            unpack_e4<false>(w.z, r + 2 * k + 4);
+            unpack_e4<false>(w.w, r + 2 * k + 6);
           }
-          put(half * 32, r);
+          if constexpr (L::kKCols == 32) tmem_st32_raw(dst, r);
+          else tmem_st16_raw(dst, r);
+        } else if (D == 128 || t < D) {                  // whole warps; lanes past D hold anything and are never read
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            const uint4 w = value_words(k);
+            unpack_e4<true>(w.x, r + 2 * k);
+            unpack_e4<true>(w.y, r + 2 * k + 2);
+            unpack_e4<true>(w.z, r + 2 * k + 4);
+            unpack_e4<true>(w.w, r + 2 * k + 6);
+          }
+          tmem_st32_raw(dst, r);
         }
-      } else if (D == 128 || t < D) {                    // whole warps; lanes past D hold anything and are never read
-        constexpr int kWordsPage = P * BITS / 32;        // words of a channel in one page: 2, 4, 8 or 16
+      } else if (keys || D == 128 || t < D) {
+        constexpr int kHalfWords = 64 * BITS / 32;       // words of 32 columns' numbers: 8 or 16
+        const int halves = keys ? L::kKCols / 32 : 2;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          if (half >= halves) break;
           uint32_t r[32];
 #pragma unroll
           for (int k = 0; k < kHalfWords; k += 4) {
-            const int word = half * kHalfWords + k, pg = word / kWordsPage;
-            uint4 w;
-            if constexpr (Y.unit == 16) {
-              w = *reinterpret_cast<const uint4*>(stage + pg * Y.page_bytes + Y.off_v + (word % kWordsPage / 4 * D + t) * 16);
-            } else {                                     // two pages of two words
-              const uint2 v0 = *reinterpret_cast<const uint2*>(stage + pg * Y.page_bytes + Y.off_v + t * 8);
-              const uint2 v1 = *reinterpret_cast<const uint2*>(stage + (pg + 1) * Y.page_bytes + Y.off_v + t * 8);
-              w = make_uint4(v0.x, v0.y, v1.x, v1.y);
-            }
+            const uint4 w = keys ? key_words(half * kHalfWords + k) : value_words(half * kHalfWords + k);
             unpack<BITS>(w.x, r + k * 16 / BITS);
             unpack<BITS>(w.y, r + (k + 1) * 16 / BITS);
             unpack<BITS>(w.z, r + (k + 2) * 16 / BITS);
             unpack<BITS>(w.w, r + (k + 3) * 16 / BITS);
           }
-          put(half * 32, r);
+          tmem_st32_raw(dst + half * 32, r);
         }
       }
       tmem_wait_st();
@@ -605,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         if (ch / kDc < p.rows && (ch & 3) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(q_at(s, ch)));
       }
     };
-    // A segment's Q as f16 of q 2^e in the order of the unpacked numbers, 2^e
+    // A segment's Q as q 2^e in f16 (or two e4m3 terms) in the order of the unpacked numbers, 2^e
     // the row's power-of-two scale; the sum of each row. Both warpgroups.
     auto q_store = [&](const Seg& s, int par) {
       uint8_t* const dst = sQ + par * L::kQBytes;
@@ -633,22 +656,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         const float up = __uint_as_float((uint32_t)(254 - ex + 7) << 23);
         if (c8 == 0) {
           s_qs[par][r] = sum;
-          s_qf[par][r] = 1.f / up;
+          s_qf[par][r] = (E4 ? 512.f : 1.f) / up;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= up;
-        const uint4 v = BITS == 4 ? make_uint4(half2_of(x[0], x[4]), half2_of(x[1], x[5]), half2_of(x[2], x[6]), half2_of(x[3], x[7]))
-                                  : make_uint4(half2_of(x[0], x[1]), half2_of(x[2], x[3]), half2_of(x[4], x[5]), half2_of(x[6], x[7]));
-        *reinterpret_cast<uint4*>(dst + (c8 >> 3) * (N * 128) + r * 128 + (((c8 & 7) ^ (r & 7)) << 4)) = v;
+        if constexpr (E4) {
+          // 8 bytes at k = 8 c8: channels 0 2 4 6 1 3 5 7; hi and lo rows may differ in r & 7
+          const Split a = split2(half2_of(x[0], x[2])), b = split2(half2_of(x[4], x[6]));
+          const Split c = split2(half2_of(x[1], x[3])), d = split2(half2_of(x[5], x[7]));
+          const int place = (c8 >> 1) << 4, sub = (c8 & 1) * 8;
+          *reinterpret_cast<uint2*>(dst + r * 128 + (place ^ ((r & 7) << 4)) + sub) = make_uint2(a.hi | b.hi << 16, c.hi | d.hi << 16);
+          *reinterpret_cast<uint2*>(dst + (NRT + r) * 128 + (place ^ (((NRT + r) & 7) << 4)) + sub) =
+              make_uint2(a.lo | b.lo << 16, c.lo | d.lo << 16);
+        } else {
+          const uint4 v = BITS == 4 ? make_uint4(half2_of(x[0], x[4]), half2_of(x[1], x[5]), half2_of(x[2], x[6]), half2_of(x[3], x[7]))
+                                    : make_uint4(half2_of(x[0], x[1]), half2_of(x[2], x[3]), half2_of(x[4], x[5]), half2_of(x[6], x[7]));
+          *reinterpret_cast<uint4*>(dst + (c8 >> 3) * (N * 128) + r * 128 + (((c8 & 7) ^ (r & 7)) << 4)) = v;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(B_QF));
     };
     // where this thread's weights go: its token's place along k
-    const int kpos = BITS == 4 ? (t & ~7) + ((t & 3) << 1) + ((t >> 2) & 1) : t;
-    uint8_t* const pw = sP + (kpos >> 6) * (N * 128) + rb * 128 + (kpos & 7) * 2;
-    const int pck = (kpos & 63) >> 3;
+    const int kpos = E4 ? (t & ~7) + ((t & 1) << 2) + ((t & 7) >> 1) : BITS == 4 ? (t & ~7) + ((t & 3) << 1) + ((t >> 2) & 1) : t;
+    uint8_t* const pw = E4 ? sP + (kpos & 15) : sP + (kpos >> 6) * (N * 128) + rb * 128 + (kpos & 7) * 2;
+    const int pck = E4 ? kpos >> 4 : (kpos & 63) >> 3;
+    const uint32_t sign = E4 && (t & 1) ? 0x80008000u : 0u;   // every other token's weights are negated
 
     // barriers of a stage's products: S^T(x) complete; O^T with x's part complete
     auto s_done = [&](int x) { return mbar_wait(BAR(B_KE + x % NB), (x / NB) & 1, &s_abort, p.status); };
@@ -684,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
 #pragma unroll
       for (int r = 0; r < NR; ++r) l[r] = corr[r] = 0.f;
       // the segment's Q sums are read after this barrier and a wait on QF: both warpgroups have stored theirs
-      sync_softmax<ALT>(wg);
+      sync_wg(wg);
       ok &= mbar_wait(BAR(B_QF), par, &s_abort, p.status);
       bool abort_all = false;
       int mine = -1;                                     // this warpgroup's last stage of the segment
@@ -710,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         }
         const float sk = __uint_as_float(kp << 16), zk = __uint_as_float(kp & 0xffff0000u);
         float sv = __uint_as_float(vp << 16);
-        float zc = __fdividef(__uint_as_float(vp & 0xffff0000u), sv) + kMid;
+        float zc = __fdividef(__uint_as_float(vp & 0xffff0000u), sv) + (E4 ? (t & 1 ? 15.f : 0.f) : kMid);
         const float ka = p.scale_log2 * sk, kb = p.scale_log2 * fmaf(kMid, sk, zk);
         if (!valid) {
           sv = 1.f;
@@ -728,21 +762,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         float s[NR];
         // s <- y + log2 s_v (- reference); hidden: -inf
         auto load_s = [&](bool with_ref) {
-#pragma unroll
-          for (int c = 0; c < NR; c += C) {
-            float y[C];
-            tm_load(tmem + lane_base + L::kColS + sb * N + rb + c, y);
-#pragma unroll
-            for (int r = 0; r < C; r += 4) {
-              const float4 qs = *reinterpret_cast<const float4*>(&s_qs[par][rb + c + r]);
-              const float4 qf = *reinterpret_cast<const float4*>(&s_qf[par][rb + c + r]);
-              float4 nu = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (with_ref) nu = *reinterpret_cast<const float4*>(&s_nu[wg][c + r]);
-              s[c + r] = fmaf(y[r] * qf.x, ka, fmaf(qs.x, kb, nu.x + lgs));
-              s[c + r + 1] = fmaf(y[r + 1] * qf.y, ka, fmaf(qs.y, kb, nu.y + lgs));
-              s[c + r + 2] = fmaf(y[r + 2] * qf.z, ka, fmaf(qs.z, kb, nu.z + lgs));
-              s[c + r + 3] = fmaf(y[r + 3] * qf.w, ka, fmaf(qs.w, kb, nu.w + lgs));
+          const uint32_t at = tmem + lane_base + L::kColS + sb * N + rb;
+          if constexpr (E4) {
+            float lo[NR];
+            if constexpr (NR == 4) {
+              tmem_ld4(at, s);
+              tmem_ld4(at + NRT, lo);
+            } else {
+              tmem_ld_cols<NR>(at, s);
+              tmem_ld_cols<NR>(at + NRT, lo);
             }
+            tmem_wait_ld();
+#pragma unroll
+            for (int r = 0; r < NR; ++r) s[r] = fmaf(lo[r], kLo, s[r]);
+          } else {
+            if constexpr (NR == 4) tmem_ld4(at, s);
+            else tmem_ld_cols<NR>(at, s);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int r = 0; r < NR; r += 4) {
+            const float4 qs = *reinterpret_cast<const float4*>(&s_qs[par][rb + r]);
+            const float4 qf = *reinterpret_cast<const float4*>(&s_qf[par][rb + r]);
+            float4 nu = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (with_ref) nu = *reinterpret_cast<const float4*>(&s_nu[wg][r]);
+            s[r] = fmaf(s[r] * qf.x, ka, fmaf(qs.x, kb, nu.x + lgs));
+            s[r + 1] = fmaf(s[r + 1] * qf.y, ka, fmaf(qs.y, kb, nu.y + lgs));
+            s[r + 2] = fmaf(s[r + 2] * qf.z, ka, fmaf(qs.z, kb, nu.z + lgs));
+            s[r + 3] = fmaf(s[r + 3] * qf.w, ka, fmaf(qs.w, kb, nu.w + lgs));
           }
           if (hide) {
 #pragma unroll
@@ -755,14 +802,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
 #pragma unroll
         for (int r = 1; r < NR; ++r) ymax = fmaxf(ymax, s[r]);
         // one barrier per stage: stop together, or raise the references together
-        const int cnt = count_softmax<ALT>(wg, !ok || ymax > kTop + kTau);
+        const int cnt = count_wg(wg, !ok || ymax > kTop + kTau);
         bool rescale_o = false;
         if (cnt > 0) {
-          if (count_softmax<ALT>(wg, !ok) > 0) { abort_all = true; break; }
+          if (count_wg(wg, !ok) > 0) { abort_all = true; break; }
           // stage maximum per row (S^T is intact until PF), then reload
           load_s(false);
           warp_part<NR, true>(s, &s_red[4 * wg], q4, lane);
-          sync_softmax<ALT>(wg);
+          sync_wg(wg);
           if (t < NR) {
             const float mx = fmaxf(fmaxf(s_red[4 * wg][t], s_red[4 * wg + 1][t]),
                                    fmaxf(s_red[4 * wg + 2][t], s_red[4 * wg + 3][t]));
@@ -771,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
             s_alpha[wg][t] = ex2(m_old - m_new);
             s_nu[wg][t] = -m_new;
           }
-          sync_softmax<ALT>(wg);
+          sync_wg(wg);
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
             const float a = s_alpha[wg][r];
@@ -788,12 +835,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         tc_fence_after();
         if (rescale_o) {
 #pragma unroll
-          for (int c = 0; c < NR; c += C) {
+          for (int c = 0; c < (E4 ? 2 * NR : NR); c += C) {   // E4: the lo columns too
             const uint32_t at = tmem + lane_base + L::kColO + (ALT ? wg * N : rb) + c;
             float o[C];
             tm_load(at, o);
 #pragma unroll
-            for (int r = 0; r < C; ++r) o[r] *= s_alpha[wg][c + r];
+            for (int r = 0; r < C; ++r) o[r] *= s_alpha[wg][(c + r) % NR];
             tm_store(at, o);
           }
           tmem_wait_st();
@@ -801,14 +848,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         uint8_t* const pb = pw + sb * L::kPBytes;
 #pragma unroll
         for (int r = 0; r < NR; r += 2) {
-          const float w0 = ex2(s[r]), w1 = ex2(s[r + 1]);
+          float w0 = ex2(s[r]), w1 = ex2(s[r + 1]);
           l[r] = fmaf(w0, rsv, l[r]);
           l[r + 1] = fmaf(w1, rsv, l[r + 1]);
+          if constexpr (E4) {
+            // the numbers' and the minima's sums meet the same rounded weight
+            w0 = round9(w0);
+            w1 = round9(w1);
+          }
           corr[r] = fmaf(w0, zc, corr[r]);
           corr[r + 1] = fmaf(w1, zc, corr[r + 1]);
           const uint32_t h = half2_of(w0, w1);
-          *reinterpret_cast<uint16_t*>(pb + r * 128 + ((pck ^ (r & 7)) << 4)) = (uint16_t)h;
-          *reinterpret_cast<uint16_t*>(pb + (r + 1) * 128 + ((pck ^ ((r + 1) & 7)) << 4)) = (uint16_t)(h >> 16);
+          if constexpr (E4) {
+            const Split sp = split2(h ^ sign);
+            pb[r * 128 + ((pck ^ (r & 7)) << 4)] = (uint8_t)sp.hi;
+            pb[(r + 1) * 128 + ((pck ^ ((r + 1) & 7)) << 4)] = (uint8_t)(sp.hi >> 8);
+            pb[(NRT + r) * 128 + ((pck ^ ((NRT + r) & 7)) << 4)] = (uint8_t)sp.lo;
+            pb[(NRT + r + 1) * 128 + ((pck ^ ((NRT + r + 1) & 7)) << 4)] = (uint8_t)(sp.lo >> 8);
+          } else {
+            *reinterpret_cast<uint16_t*>(pb + r * 128 + ((pck ^ (r & 7)) << 4)) = (uint16_t)h;
+            *reinterpret_cast<uint16_t*>(pb + (r + 1) * 128 + ((pck ^ ((r + 1) & 7)) << 4)) = (uint16_t)(h >> 16);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -820,13 +880,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       // ---- the next segment's Q goes to the other buffer: the products of
       // the segment before this one are done (this warpgroup has waited for a
       // later one, or for its last), and its sums have been read by the other
-      // warpgroup (ALT: the merge of that segment, waited for here or below)
-      if (ALT && wg == 1 && seg > 0) ok &= mbar_wait(BAR(B_Y), (seg - 1) & 1, &s_abort, p.status);
+      // warpgroup (which has met this one at that segment's end, here or below)
+      if (wg == 1 && seg > 0) ok &= mbar_wait(BAR(B_Y), (seg - 1) & 1, &s_abort, p.status);
       if (has_next) q_store(nx, par ^ 1);
       // ---- segment epilogue: row sums, then (O^T + corr) / l
       warp_part<NR, false>(l, &s_red[4 * wg], q4, lane);
       warp_part<NR, false>(corr, &s_red2[4 * wg], q4, lane);
-      sync_softmax<ALT>(wg);
+      sync_wg(wg);
       if (t < NR) {
         const float (*a)[32] = &s_red[4 * wg], (*c)[32] = &s_red2[4 * wg];
         s_sum[wg][t] = (a[0][t] + a[1][t]) + (a[2][t] + a[3][t]);
@@ -834,11 +894,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       }
       if (mine >= 0) ok &= o_done(mine);                 // PV of the last stage
       tc_fence_after();
-      sync_softmax<ALT>(wg);
+      sync_wg(wg);
       float* const sX = reinterpret_cast<float*>(dyn + L::kOffX);
       // rows c .. c + C of this thread's channel
       auto load_o = [&](int c, float* o) {
-        tm_load(tmem + lane_base + L::kColO + (ALT ? wg * N : rb) + c, o);
+        const uint32_t at = tmem + lane_base + L::kColO + (ALT ? wg * N : rb) + c;
+        tm_load(at, o);
+        if constexpr (E4) {
+          float lo[C];
+          tm_load(at + NRT, lo);
+#pragma unroll
+          for (int r = 0; r < C; ++r) o[r] = fmaf(lo[r], kLo, o[r]) * 512.f;
+        }
 #pragma unroll
         for (int r = 0; r < C; ++r) o[r] += s_corr[wg][c + r];
       };
@@ -864,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         const bool single = sg.nseg == 1;
         const int slot_idx = sg.unit + blockIdx.x;       // partial slot of (unit, this CTA)
         const size_t rowbase = (size_t)(sg.b * p.R + p.r0) * p.Hq + (size_t)sg.h * p.G;
-        if (ALT) ok &= mbar_wait(BAR(B_X), par, &s_abort, p.status);
+        if (ALT) ok &= mbar_wait(BAR(B_X), par, &s_abort, p.status);   // the second warpgroup's part
         if (t < NR) {
           // one state from one or two: a warpgroup without tokens has sum 0
           const int i = rb + t;
@@ -889,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           }
           s_sum[wg][t] = lt == 0.f ? 0.f : 1.f / lt;
         }
-        sync_softmax<ALT>(wg);
+        sync_wg(wg);
 #pragma unroll
         for (int c = 0; c < NR; c += C) {
           float o[C];
@@ -914,15 +981,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           }
         }
         tc_fence_before();
-        if (ALT) {
-          __syncwarp();
+        if (!single) __threadfence();
+        __syncwarp();
+        if (!ALT && wg == 1) {
+          if (lane == 0) mbar_arrive(BAR(B_X));          // its rows are written
+        } else {
+          if (!ALT) ok &= mbar_wait(BAR(B_X), par, &s_abort, p.status);
           if (lane == 0) mbar_arrive(BAR(B_Y));
         }
-        if (!single) {
-          __threadfence();
-          sync_softmax<ALT>(wg);
-          if (tid == 0) s_ticket = atomicAdd(p.tickets + sg.unit, 1u);
-          sync_softmax<ALT>(wg);
+        if (!single && wg == 0) {
+          sync_wg(wg);
+          if (tid == 0) {
+            __threadfence();
+            s_ticket = atomicAdd(p.tickets + sg.unit, 1u);
+          }
+          sync_wg(wg);
           if (s_ticket == sg.nseg - 1) {
             // this CTA finished the unit last: merge its partials after the
             // CTA's own streaming is done (immediately if the list is full)
@@ -930,9 +1003,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
               if (tid == 0) s_pend[s_npend] = make_int4(sg.b, sg.h, sg.first_cta + sg.unit, sg.nseg);
             } else {
               __threadfence();
-              kvq_combine<__nv_bfloat16>(p, sg.b, sg.h, sg.first_cta + sg.unit, sg.nseg, ALT ? 128 : 256);
+              kvq_combine<__nv_bfloat16>(p, sg.b, sg.h, sg.first_cta + sg.unit, sg.nseg, 128);
             }
-            sync_softmax<ALT>(wg);
+            sync_wg(wg);
             if (tid == 0) {
               if (s_npend < kMaxPend) ++s_npend;
               p.tickets[sg.unit] = 0u;
@@ -940,17 +1013,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           }
         }
       }
-      sync_softmax<ALT>(wg);                             // s_alpha / s_nu / s_sum reads done
+      sync_wg(wg);                             // s_alpha / s_nu / s_sum reads done
       x = sg.end;
       sg = nx;
     }
     // ---- deferred merges of the units this CTA finished last (skipped,
     // together, after a failed wait)
-    if ((!ALT || wg == 0) && count_softmax<ALT>(wg, !ok) == 0) {
+    if (wg == 0 && count_wg(wg, !ok) == 0) {
       __threadfence();
       for (int k = 0; k < s_npend; ++k) {
         const int4 u = s_pend[k];
-        kvq_combine<__nv_bfloat16>(p, u.x, u.y, u.z, u.w, ALT ? 128 : 256);
+        kvq_combine<__nv_bfloat16>(p, u.x, u.y, u.z, u.w, 128);
       }
     }
   }
@@ -959,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kMma) {
+  if (warp == kMmaQk) {
     tc_fence_after();
     if (lane == 0) mbar_wait_drain(BAR(B_TD), 0, p.status);
     __syncwarp();
@@ -984,12 +1057,13 @@ cudaError_t launch_one(const KvqAttnParams& p, cudaStream_t st) {
   return launch_kernel(attn_kernel<NR, ALT, D, P, BITS>, dim3(grid), dim3(kThreads), smem, st, 1, p);
 }
 
-// Rows of a softmax warpgroup: the packed rows rounded up; beyond 16, half of them.
+// Rows of a softmax warpgroup: the packed rows rounded up; beyond 24, half of them.
 template <int D, int P, int BITS>
 cudaError_t launch_rows(const KvqAttnParams& p, cudaStream_t st) {
   if (p.rows <= 4) return launch_one<4, true, D, P, BITS>(p, st);
   if (p.rows <= 8) return launch_one<8, true, D, P, BITS>(p, st);
   if (p.rows <= 16) return launch_one<16, true, D, P, BITS>(p, st);
+  if (p.rows <= 24) return launch_one<24, true, D, P, BITS>(p, st);
   if (p.rows <= 32) return launch_one<16, false, D, P, BITS>(p, st);
   if (p.rows <= 48) return launch_one<24, false, D, P, BITS>(p, st);
   return launch_one<32, false, D, P, BITS>(p, st);

@@ -12,9 +12,12 @@ N = 2^bits - 1, c = N / 2, T tokens):
   each of D values off by at most 2^-32 of the row's largest, times scale s_k N.
   With the base-2 exponential's 2^-21 relative error a weight is off by e + 2^-21 +
   4 u |score| of itself, which moves the output by at most twice that times A;
-- bf16: a weight w = p s_v is rounded to float16: off by at most 2^-12 w + 2^-25, where the row's largest weight is at
-  least 2^8; the error meets n - c, at most c + 1 in size: (c + 1) (2^-12 B + T 2^-33 max s_v); the output's rounding
-  is 2^-8 |out|;
+- bf16, 8 bits or more than 24 packed rows: a weight w = p s_v is rounded to float16: off by at most 2^-12 w + 2^-25,
+  where the row's largest weight is at least 2^8; the error meets n - c, at most c + 1 in size: (c + 1) (2^-12 B + T
+  2^-33 max s_v). 4 bits, up to 24 packed rows: w is rounded to 9 bits, which moves the
+  output by at most 2^-9 A, and held in two e4m3 terms, off by at most 2^-15 where the row's largest is at
+  least 2^6, which meets n: N T 2^-21 max s_v; a query's two terms leave at most 2^-15 of a value where the row's
+  largest is at least 128: D values of 2^-22 of the row's largest, times scale s_k N. The output's rounding is 2^-8 |out|;
 - sums over T tokens: at most T + 64 roundings of partial sums no larger than 2 (N + 1) B + A.
 The log-sum-exp is off by at most max e + 2^-21 + (T + 64) u + 4 u |lse|."""
 import numpy as np
@@ -91,14 +94,18 @@ class Case:
             sumq = np.abs(q.astype(np.float64)).sum(-1)                         # [R, Hq]
             span = (held["sk"] * (N + 1) + np.abs(held["zk"])).max(0).repeat(self.G)   # [Hq]
             e = (32 + self.D / 4) * U * self.scale * span * sumq
+            e4 = self.dtype == "bf16" and self.bits == 4 and self.G * self.rows <= 24
             if self.dtype == "bf16":
-                e = e + self.D * 2.0 ** -32 * np.abs(q).max(-1) * self.scale * N * held["sk"].max(0).repeat(self.G)
+                e = e + (self.D * 2.0 ** (-22 if e4 else -32) * np.abs(q).max(-1) * self.scale * N
+                         * held["sk"].max(0).repeat(self.G))
             top = np.where(np.isfinite(lse), np.abs(lse), 0.0)
             w = e + 2.0 ** -21 + 4 * U * (top + np.log(max(T, 1)) + 1)
             tol = 2 * w[..., None] * A + (T + 64) * U * (2 * (N + 1) * B[..., None] + A) + 1e-30
+            big = T * held["sv"].max(0).repeat(self.G)[None, :, None]
             if self.dtype == "bf16":
-                few = T * 2.0 ** -33 * held["sv"].max(0).repeat(self.G)[None, :, None]
-                tol = tol + 1.01 * ((N / 2 + 1) * (2.0 ** -12 * B[..., None] + few) + 2.0 ** -8 * np.abs(ref))
+                tol = tol + 1.01 * 2.0 ** -8 * np.abs(ref)
+                tol = tol + 1.01 * (2.0 ** -9 * A + N * 2.0 ** -21 * big if e4
+                                    else (N / 2 + 1) * (2.0 ** -12 * B[..., None] + 2.0 ** -33 * big))
             out, got = self.out[b].double().cpu().numpy(), self.lse[b].double().cpu().numpy()
             bad = np.abs(out - ref) > tol
             assert not bad.any(), (b, np.argwhere(bad)[:3], out[bad][:3], ref[bad][:3], tol[bad][:3])
@@ -392,7 +399,10 @@ def test_a_run_of_the_calls_together(bits):
             held = Q.held_rows(host, table[b], hl[b], D, P, bits)
             ref, rl, A, B = Q.attend(q[b].float().cpu().numpy(), held, 0.09, rows)
             # the weights' and the output's roundings as above; scores and float32 sums are far below 2^-10 of A
+            few = 15 * hl[b] * 2.0 ** -21 * held["sv"].max()
             tol = 1.01 * (2 ** (bits - 1) * 2.0 ** -12 * B[..., None] + 2.0 ** -8 * np.abs(ref)) + 2.0 ** -10 * A
+            if bits == 4:
+                tol = tol + 1.01 * 2.0 ** -9 * A + few
             assert (np.abs(out[b].double().cpu().numpy() - ref) <= tol).all()
             assert np.abs(lse[b].double().cpu().numpy() - rl).max() < 1e-3
 
