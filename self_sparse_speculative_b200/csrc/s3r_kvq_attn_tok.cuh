@@ -411,69 +411,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     // ======================================================= producer warp
     if (p.page_list) pdl_wait();
     const uint64_t pol = l2_policy_evict_first();
-    // page-id windows of 32 flattened positions: lane k of a window holds
-    // position wbase + k. w0 = in use, w1 = page ids in flight, w2 = logical pages
-    // in flight.
-    int w0_lp, w0_ph, w1_lp, w1_ph, w2_lp, w2_u, u;
-    auto phys_load = [&](int lp, int unit) {
-      if (lp == -1) return -1;
-      const int b = unit / p.Hkv;
-      const int n_b = (p.context_lens[b] + P - 1) / P;
-      if (lp < 0 || lp >= n_b) { flag_status(p.status, S3R_DEV_BAD_PAGE_ID); return -1; }
-      const int ph = p.block_table[(size_t)b * p.max_pages + lp];
-      if (ph < 0 || ph >= p.num_pages_total) { flag_status(p.status, S3R_DEV_BAD_PAGE_ID); return -1; }
-      return ph;
+    // Pages in batches of 32 of one segment, a lane each: the lane that looked
+    // a page up copies it, and the next batch's ids are in flight meanwhile.
+    auto look_up = [&](const Seg& s, int k, int* lp, int* ph) {
+      *lp = *ph = -1;
+      if (k + lane >= s.npg) return;
+      *lp = p.page_list ? p.page_list[(size_t)s.unit * p.budget + s.k0 + k + lane] : s.k0 + k + lane;
+      bool there = *lp >= 0;
+      if (p.page_list) there = there && *lp < (p.context_lens[s.b] + P - 1) / P;
+      if (there) *ph = p.block_table[(size_t)s.b * p.max_pages + *lp];
     };
-    int wbase = lo;
-    page_of(p, s_prefix, wbase + lane, hi, W, &w0_lp, &u);
-    w0_ph = phys_load(w0_lp, u);
-    page_of(p, s_prefix, wbase + 32 + lane, hi, W, &w1_lp, &u);
-    w1_ph = phys_load(w1_lp, u);
-    page_of(p, s_prefix, wbase + 64 + lane, hi, W, &w2_lp, &w2_u);
-    bool waited = p.page_list != nullptr;
-    int g = 0;
-    bool ok = true;
-    for (int x = lo; x < hi && ok;) {
-      const Seg sg = locate(p, s_prefix, x, hi, W);
-      const int nst = (sg.npg + ppt - 1) / ppt;
-      for (int j = 0; j < nst; ++j, ++g) {
+    bool waited = p.page_list != nullptr, ok = true, more = true;
+    int g = 0, k = 0, lp, ph;
+    Seg sg = locate(p, s_prefix, lo, hi, W);
+    look_up(sg, 0, &lp, &ph);
+    while (more && ok) {
+      Seg nx = sg;
+      int nk = k + 32, nlp = -1, nph = -1;
+      if (nk >= sg.npg) {
+        nk = 0;
+        more = sg.end < hi;
+        if (more) nx = locate(p, s_prefix, sg.end, hi, W);
+      }
+      if (more) look_up(nx, nk, &nlp, &nph);
+      if (lp != -1 && (ph < 0 || ph >= p.num_pages_total)) {
+        flag_status(p.status, S3R_DEV_BAD_PAGE_ID);
+        ph = -1;
+      }
+      const unsigned real = __ballot_sync(0xffffffffu, ph >= 0);
+      const int stages = (min(32, sg.npg - k) + ppt - 1) / ppt;
+      const uint8_t* const src = p.pages + ((size_t)max(ph, 0) * p.Hkv + sg.h) * Y.page_bytes;
+      for (int j = 0; j < stages; ++j, ++g) {
         const int st = g % NS;
         if (g == NS && !waited) {                        // the ring's first fill goes out before it
           pdl_wait();
           waited = true;
         }
-        int my_lp = -1, my_ph = -1;
-        for (int pp = 0; pp < ppt; ++pp) {
-          // positions past the segment belong to the next one: the windows
-          // must not move past its first page (warp-uniform)
-          if (j * ppt + pp >= sg.npg) break;
-          const int xp = x + j * ppt + pp;
-          while (xp >= wbase + 32) {                     // advance the windows (warp-uniform)
-            wbase += 32;
-            w0_lp = w1_lp; w0_ph = w1_ph;
-            w1_lp = w2_lp;
-            w1_ph = phys_load(w1_lp, w2_u);
-            page_of(p, s_prefix, wbase + 64 + lane, hi, W, &w2_lp, &w2_u);
-          }
-          const int src = xp - wbase;
-          const int lp = __shfl_sync(0xffffffffu, w0_lp, src & 31);
-          const int ph = __shfl_sync(0xffffffffu, w0_ph, src & 31);
-          if (lane == pp) { my_lp = lp; my_ph = ph; }
-        }
         if (!__all_sync(0xffffffffu, mbar_wait(BAR(B_EMPTY + st), ((g / NS) & 1) ^ 1, &s_abort, p.status))) {
           ok = false;
           break;
         }
-        if (lane < 8) s_stage_lp[st][lane] = my_ph >= 0 ? my_lp : -1;
-        const unsigned real = __ballot_sync(0xffffffffu, my_ph >= 0);
+        const bool here = lane / ppt == j;
+        if (here) s_stage_lp[st][lane % ppt] = ph >= 0 ? lp : -1;
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(BAR(B_FULL + st), (uint32_t)__popc(real) * Y.page_bytes);
+        if (lane == 0)
+          mbar_arrive_expect_tx(BAR(B_FULL + st), (uint32_t)__popc((real >> (j * ppt)) & ((1u << ppt) - 1u)) * Y.page_bytes);
         __syncwarp();
-        if (my_ph >= 0)
-          bulk_load_hint(aKV + st * L::kStage + lane * Y.page_bytes,
-                         p.pages + ((size_t)my_ph * p.Hkv + sg.h) * Y.page_bytes, Y.page_bytes, BAR(B_FULL + st), pol);
+        if (here && ph >= 0)
+          bulk_load_hint(aKV + st * L::kStage + (lane % ppt) * Y.page_bytes, src, Y.page_bytes, BAR(B_FULL + st), pol);
       }
-      x = sg.end;
+      sg = nx;
+      k = nk;
+      lp = nlp;
+      ph = nph;
     }
     if (!waited) pdl_wait();
     // drain: wait until every issued copy has landed
