@@ -31,8 +31,8 @@
 // times the packed bytes, never crosses shared memory. Q and w are the B
 // operands in shared memory.
 //
-// Warps: two softmax warpgroups (thread = token), two unpacking ones (keys,
-// values), one producer (a bulk copy per (page, head) into an NS-stage ring of
+// Warps: two softmax warpgroups (thread = token), two unpacking ones (on
+// alternate stages), one producer (a bulk copy per (page, head) into an NS-stage ring of
 // 128 tokens), one MMA issuer per product. A stage's softmax is a chain of
 // waits and latencies of about 1500 cycles, twice what a stage's bytes take, so
 // up to 24 rows the warpgroups take alternate stages (ALT): each keeps its own
@@ -58,6 +58,7 @@ namespace s3r {
 namespace kvq {
 
 constexpr int kTok = 128;                    // tokens per stage
+constexpr int kHidden = 0x7fffffff;
 constexpr float kNuInit = 1e30f;             // -(reference) before the first score of a segment
 constexpr int kSmemBudget = 232448 - 10240;  // beside the static arrays
 constexpr int kMaxPend = 8;                  // deferred merges of units per CTA
@@ -81,20 +82,22 @@ struct Lay {
   static constexpr uint32_t kStage = 2 * (kTok * D * BITS / 8) + 8 * kTok;
   static constexpr uint32_t kOffP = 2 * kQBytes;
   static constexpr uint32_t kOffX = kOffP + 2 * kPBytes;
-  static constexpr uint32_t kOffKV = kOffX + kXBytes;
+  // TMEM columns: NB key tiles, NB value tiles, S^T[NSB], O^T[1 or 2]
+  static constexpr int kO = ALT ? 2 : 1;
+  static constexpr int NSB = 4 * kTile + (4 + kO) * N <= 512 ? 4 : 2;
+  static constexpr int NB = 8 * kTile + (NSB + kO) * N <= 512 ? 4 : 2;
+  static constexpr int NKE = NB > NSB ? NB : NSB;          // products of keys whose completion may still be waited for
+  static constexpr uint32_t kColK = 0, kColV = kTile * NB, kColS = 2 * kTile * NB, kColO = kColS + NSB * N;
+  static constexpr uint32_t kOffT = kOffX + kXBytes;       // tokens' parameters, NB stages: float4 [128], float2 [128]
+  static constexpr uint32_t kOffKV = kOffT + NB * 128 * 24;
   static constexpr int kNSraw = (kSmemBudget - (int)kOffKV - 1024) / (int)kStage;
-  static constexpr int kNS = kNSraw > 12 ? 12 : kNSraw;
+  static constexpr int kNS = kNSraw >= 8 ? 8 : kNSraw >= 4 ? 4 : 2;   // ring sizes are powers of two
   static constexpr uint32_t kDynBytes = kOffKV + kNS * kStage + 1024;
-  // TMEM columns: NB key tiles, NB value tiles, S^T[2], O^T[1 or 2]
-  static constexpr int kAcc = ALT ? 4 : 3;
-  static constexpr int kNBraw = (512 - kAcc * N) / (2 * kTile);
-  static constexpr int NB = kNBraw > 4 ? 4 : kNBraw;
-  static constexpr uint32_t kColK = 0, kColV = kTile * NB, kColS = 2 * kTile * NB, kColO = kColS + 2 * N;
   // log2 of the largest weight when a row's reference is raised, and the
   // slack before it is raised again: weights stay below 256 or 2^15
   static constexpr float kTop = E4 ? 6.f : 8.f, kTau = E4 ? 2.f : 7.f;
-  static_assert(kNS >= 2 && NB >= 2, "the rings need two stages");
-  static_assert(2 * kTile * NB + kAcc * N <= 512, "TMEM columns");
+  static_assert(kNSraw >= 2, "the ring needs two stages");
+  static_assert(2 * kTile * NB + (NSB + kO) * N <= 512, "TMEM columns");
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, f32 accumulate: 32 of k of e4m3 or 16 of f16.
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   using L = Lay<NR, ALT, D, BITS>;
   constexpr KvqLayout Y = kvq_layout(D, P, BITS);
   constexpr int kUnit = Y.unit;                          // bytes of a V piece
-  constexpr int NRT = L::NRT, N = L::N, NB = L::NB, NS = L::kNS;
+  constexpr int NRT = L::NRT, N = L::N, NB = L::NB, NS = L::kNS, NSB = L::NSB, NKE = L::NKE;
   constexpr int ppt = kTok / P;                          // pages per stage
   constexpr bool E4 = L::E4;
   constexpr float kTop = L::kTop, kTau = L::kTau;
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   static_assert(ppt * Y.page_bytes == (int)L::kStage, "stage bytes");
   extern __shared__ __align__(1024) uint8_t dyn_raw[];
   uint8_t* dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t s_bar[2 * NS + 4 * NB + 6];
+  __shared__ __align__(8) uint64_t s_bar[2 * NS + 2 * NB + NKE + NSB + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_ticket;
@@ -368,11 +371,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
 
   const uint32_t bar0 = smem_addr(&s_bar[0]);
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-  // KF / VF: an unpacked tile of keys / values is in TMEM; KE / VE: its
-  // product is done (the tile is free; S^T / O^T has its part): tile k uses
-  // barrier k % NB; PF: w(g) is written (and S^T(g) read), by parity of g
-  constexpr int B_FULL = 0, B_EMPTY = NS, B_KF = 2 * NS, B_KE = B_KF + NB, B_VF = B_KE + NB, B_VE = B_VF + NB,
-                B_PF = B_VE + NB, B_QF = B_PF + 2, B_TD = B_QF + 1, B_X = B_TD + 1, B_Y = B_X + 1;
+  // UF: a stage is unpacked (both tiles in TMEM, token parameters in shared
+  // memory); KE / VE: its product of keys / values is done (S^T / O^T has its
+  // part; VE: tiles and parameters are free); PF: w(g) is written (and S^T(g)
+  // and the parameters read). Stage g uses barrier g % size of each ring, and each
+  // ring is as long as the stages between a completion and its last waiter, so
+  // that none is two phases ahead of a wait.
+  constexpr int B_FULL = 0, B_EMPTY = NS, B_UF = 2 * NS, B_KE = B_UF + NB, B_VE = B_KE + NKE,
+                B_PF = B_VE + NB, B_QF = B_PF + NSB, B_TD = B_QF + 1, B_X = B_TD + 1, B_Y = B_X + 1;
   uint8_t* sQ = dyn;
   uint8_t* sP = dyn + L::kOffP;
   uint8_t* sKV = dyn + L::kOffKV;
@@ -385,15 +391,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(BAR(B_FULL + i), 1);
-      mbar_init(BAR(B_EMPTY + i), ALT ? 12 : 16);        // every warp that reads the stage
+      mbar_init(BAR(B_EMPTY + i), 4);                    // the warps that unpack the stage
     }
     for (int i = 0; i < NB; ++i) {
-      mbar_init(BAR(B_KF + i), 4);
-      mbar_init(BAR(B_KE + i), 1);
-      mbar_init(BAR(B_VF + i), 4);
+      mbar_init(BAR(B_UF + i), 4);
       mbar_init(BAR(B_VE + i), 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(BAR(B_PF + i), ALT ? 4 : 8);
+    for (int i = 0; i < NKE; ++i) mbar_init(BAR(B_KE + i), 1);
+    for (int i = 0; i < NSB; ++i) mbar_init(BAR(B_PF + i), ALT ? 4 : 8);
     mbar_init(BAR(B_QF), 8);
     mbar_init(BAR(B_TD), 2);
     mbar_init(BAR(B_X), 4);
@@ -476,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     // then costs 10 cycles to issue instead of 46 from a lane's own branch
     // (N = 16, measured), and a commit about 80 - there is one per tile, which
     // both the unpacking warps (tile free) and the softmax (product done) wait on.
-    // QK(g) needs its keys, w(g - 2) written (S^T buffer g & 1 has been read)
-    // and first in a segment the segment's Q; PV(g) needs w(g) and its values.
+    // QK(g) needs its stage unpacked, w(g - NSB) written (S^T buffer g % NSB has been read)
+    // and first in a segment the segment's Q; PV(g) needs w(g).
     constexpr uint32_t idesc = idesc_f32(128, N);
     auto uni = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
     const uint32_t tm = uni(tmem);
@@ -489,13 +494,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     for (Cursor c = cursor_begin(p, s_prefix, lo, hi, W, ppt); uni(c.valid); cursor_next(p, s_prefix, hi, W, ppt, c)) {
       const int buf = c.g % NB;
       if (warp == kMmaQk) {
-        bool ok = mbar_wait(BAR(B_KF + buf), (c.g / NB) & 1, &s_abort, p.status);
-        if (c.g >= 2) ok = ok && mbar_wait(BAR(B_PF + (c.g & 1)), ((c.g >> 1) & 1) ^ 1, &s_abort, p.status);
+        bool ok = mbar_wait(BAR(B_UF + buf), (c.g / NB) & 1, &s_abort, p.status);
+        if (c.g >= NSB) ok = ok && mbar_wait(BAR(B_PF + c.g % NSB), (c.g / NSB - 1) & 1, &s_abort, p.status);
         if (c.j == 0) ok = ok && mbar_wait(BAR(B_QF), c.s & 1, &s_abort, p.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const uint32_t d = uni(tm + L::kColS + (c.g & 1) * N), a = uni(tm + L::kColK + buf * L::kTile);
-        const uint32_t bar = uni(BAR(B_KE + buf)), step = uni((c.s & 1) * (L::kQBytes >> 4));
+        const uint32_t d = uni(tm + L::kColS + c.g % NSB * N), a = uni(tm + L::kColK + buf * L::kTile);
+        const uint32_t bar = uni(BAR(B_KE + c.g % NKE)), step = uni((c.s & 1) * (L::kQBytes >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < L::kKCols / 8; ++kk)
@@ -503,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           umma_commit(bar);
         }
       } else {
-        bool ok = mbar_wait(BAR(B_VF + buf), (c.g / NB) & 1, &s_abort, p.status);
-        ok = ok && mbar_wait(BAR(B_PF + (c.g & 1)), (c.g >> 1) & 1, &s_abort, p.status);
+        bool ok = mbar_wait(BAR(B_UF + buf), (c.g / NB) & 1, &s_abort, p.status);
+        ok = ok && mbar_wait(BAR(B_PF + c.g % NSB), (c.g / NSB) & 1, &s_abort, p.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const uint32_t d = uni(tm + L::kColO + (ALT ? (c.g & 1) * N : 0)), a = uni(tm + L::kColV + buf * L::kTile);
@@ -523,79 +528,121 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     __syncwarp();
   } else if (warp >= 8) {
     // ======================================================= unpacking warps
+    // The warpgroups take alternate stages, keys and values, so that a
+    // warpgroup's chain of waits, loads and stores spans two stages. The tiles
+    // and parameters of stage g - NB are free once its product of values is
+    // done: its product of keys and its softmax came before.
     split_registers<false>();
-    const bool keys = warp < 12;
+    const int uwg = (warp - 8) >> 2;
     const int t = tid & 127;                             // TMEM lane: token of S^T, channel of O^T
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
-    const int b_free = keys ? B_KE : B_VE, b_ready = keys ? B_KF : B_VF;
+    constexpr int kWordsPage = P * BITS / 32;            // words of a channel in one page: 2, 4, 8 or 16
+    constexpr int kHalfWords = 64 * BITS / 32;           // f16: words of 32 columns' numbers, 8 or 16
     Cursor c = cursor_begin(p, s_prefix, lo, hi, W, ppt);
+    int Lb = -1, of = -1;                                // length of sequence `of`
     for (; c.valid; cursor_next(p, s_prefix, hi, W, ppt, c)) {
-      const int st = c.g % NS, buf = c.g % NB;
-      bool ok = mbar_wait(BAR(B_FULL + st), (c.g / NS) & 1, &s_abort, p.status);
-      ok = ok && mbar_wait(BAR(b_free + buf), ((c.g / NB) & 1) ^ 1, &s_abort, p.status);
+      const uint32_t g = (uint32_t)c.g, st = g % NS, buf = g % NB;
+      if ((g & 1u) != (uint32_t)uwg) continue;
+      if (of != c.sg.b) {
+        of = c.sg.b;
+        Lb = p.context_lens[of];
+      }
+      bool ok = mbar_wait(BAR(B_FULL + st), (g / NS) & 1, &s_abort, p.status);
+      if (g >= NB) ok = ok && mbar_wait(BAR(B_VE + buf), (g / NB - 1) & 1, &s_abort, p.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const uint8_t* stage = sKV + st * L::kStage;
-      const uint32_t dst = tmem + lane_base + (keys ? L::kColK : L::kColV) + buf * L::kTile;
-      const uint8_t* row = stage + (t / P) * Y.page_bytes + (t % P) * 16;
-      constexpr int kWordsPage = P * BITS / 32;          // words of a channel in one page: 2, 4, 8 or 16
-      // words k .. k + 3 of this token's channels / of this channel's tokens
-      auto key_words = [&](int k) { return *reinterpret_cast<const uint4*>(row + (k / 4) * (P * 16)); };
-      auto value_words = [&](int k) {
-        const int pg = k / kWordsPage;
-        if constexpr (kUnit == 16)
-          return *reinterpret_cast<const uint4*>(stage + pg * Y.page_bytes + Y.off_v + (k % kWordsPage / 4 * D + t) * 16);
-        const uint2 v0 = *reinterpret_cast<const uint2*>(stage + pg * Y.page_bytes + Y.off_v + t * 8);   // two pages of two words
-        const uint2 v1 = *reinterpret_cast<const uint2*>(stage + (pg + 1) * Y.page_bytes + Y.off_v + t * 8);
-        return make_uint4(v0.x, v0.y, v1.x, v1.y);
-      };
-      if constexpr (E4) {
-        uint32_t r[32];
-        if (keys) {
+      const uint8_t* const stage = sKV + st * L::kStage;
+      {
+        const uint32_t dst = tmem + lane_base + L::kColK + buf * L::kTile;
+        const uint8_t* const row = stage + (t / P) * Y.page_bytes + (t % P) * 16;
+        auto words = [&](int k) { return *reinterpret_cast<const uint4*>(row + (k / 4) * (P * 16)); };
 #pragma unroll
-          for (int k = 0; k < L::kKCols / 2; k += 4) {
-            const uint4 w = key_words(k);
-            unpack_e4<false>(w.x, r + 2 * k);
-            unpack_e4<false>(w.y, r + 2 * k + 2);
-            unpack_e4<false>(w.z, r + 2 * k + 4);
-            unpack_e4<false>(w.w, r + 2 * k + 6);
-          }
-          if constexpr (L::kKCols == 32) tmem_st32_raw(dst, r);
-          else tmem_st16_raw(dst, r);
-        } else if (D == 128 || t < D) {                  // whole warps; lanes past D hold anything and are never read
-#pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const uint4 w = value_words(k);
-            unpack_e4<true>(w.x, r + 2 * k);
-            unpack_e4<true>(w.y, r + 2 * k + 2);
-            unpack_e4<true>(w.z, r + 2 * k + 4);
-            unpack_e4<true>(w.w, r + 2 * k + 6);
-          }
-          tmem_st32_raw(dst, r);
-        }
-      } else if (keys || D == 128 || t < D) {
-        constexpr int kHalfWords = 64 * BITS / 32;       // words of 32 columns' numbers: 8 or 16
-        const int halves = keys ? L::kKCols / 32 : 2;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half >= halves) break;
+        for (int half = 0; half < L::kKCols / 32 || half < 1; ++half) {
           uint32_t r[32];
+          if constexpr (E4) {
 #pragma unroll
-          for (int k = 0; k < kHalfWords; k += 4) {
-            const uint4 w = keys ? key_words(half * kHalfWords + k) : value_words(half * kHalfWords + k);
-            unpack<BITS>(w.x, r + k * 16 / BITS);
-            unpack<BITS>(w.y, r + (k + 1) * 16 / BITS);
-            unpack<BITS>(w.z, r + (k + 2) * 16 / BITS);
-            unpack<BITS>(w.w, r + (k + 3) * 16 / BITS);
+            for (int k = 0; k < L::kKCols / 2; k += 4) {
+              const uint4 w = words(k);
+              unpack_e4<false>(w.x, r + 2 * k);
+              unpack_e4<false>(w.y, r + 2 * k + 2);
+              unpack_e4<false>(w.z, r + 2 * k + 4);
+              unpack_e4<false>(w.w, r + 2 * k + 6);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kHalfWords; k += 4) {
+              const uint4 w = words(half * kHalfWords + k);
+              unpack<BITS>(w.x, r + k * 16 / BITS);
+              unpack<BITS>(w.y, r + (k + 1) * 16 / BITS);
+              unpack<BITS>(w.z, r + (k + 2) * 16 / BITS);
+              unpack<BITS>(w.w, r + (k + 3) * 16 / BITS);
+            }
+          }
+          if constexpr (L::kKCols >= 32) tmem_st32_raw(dst + half * 32, r);
+          else tmem_st16_raw(dst, r);
+        }
+      }
+      if (D == 128 || t < D) {                           // whole warps; lanes past D hold anything and are never read
+        const uint32_t dst = tmem + lane_base + L::kColV + buf * L::kTile;
+        auto words = [&](int k) {
+          const int pg = k / kWordsPage;
+          if constexpr (kUnit == 16)
+            return *reinterpret_cast<const uint4*>(stage + pg * Y.page_bytes + Y.off_v + (k % kWordsPage / 4 * D + t) * 16);
+          const uint2 v0 = *reinterpret_cast<const uint2*>(stage + pg * Y.page_bytes + Y.off_v + t * 8);   // two pages of two words
+          const uint2 v1 = *reinterpret_cast<const uint2*>(stage + (pg + 1) * Y.page_bytes + Y.off_v + t * 8);
+          return make_uint4(v0.x, v0.y, v1.x, v1.y);
+        };
+#pragma unroll
+        for (int half = 0; half < L::kTile / 32; ++half) {
+          uint32_t r[32];
+          if constexpr (E4) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              const uint4 w = words(k);
+              unpack_e4<true>(w.x, r + 2 * k);
+              unpack_e4<true>(w.y, r + 2 * k + 2);
+              unpack_e4<true>(w.z, r + 2 * k + 4);
+              unpack_e4<true>(w.w, r + 2 * k + 6);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kHalfWords; k += 4) {
+              const uint4 w = words(half * kHalfWords + k);
+              unpack<BITS>(w.x, r + k * 16 / BITS);
+              unpack<BITS>(w.y, r + (k + 1) * 16 / BITS);
+              unpack<BITS>(w.z, r + (k + 2) * 16 / BITS);
+              unpack<BITS>(w.w, r + (k + 3) * 16 / BITS);
+            }
           }
           tmem_st32_raw(dst + half * 32, r);
         }
+      }
+      // the token's parameters for the softmax: y = ka S^T + kb sum q (scaled),
+      // log2 s_v, 1 / s_v, the centre of its values over s_v, and its position
+      // against the rows' (hidden from rows before `excess`; from all: kHidden)
+      {
+        const uint8_t* pg = stage + (t / P) * Y.page_bytes;
+        const uint32_t kp = *reinterpret_cast<const uint32_t*>(pg + Y.off_kp + (t % P) * 4);
+        const uint32_t vp = *reinterpret_cast<const uint32_t*>(pg + Y.off_vp + (t % P) * 4);
+        const int lp = s_stage_lp[st][t / P];
+        const int pos = lp * P + (t % P);
+        const bool valid = lp >= 0 && pos < Lb;
+        const float sk = __uint_as_float(kp << 16), zk = __uint_as_float(kp & 0xffff0000u);
+        const float sv = valid ? __uint_as_float(vp << 16) : 1.f;
+        const float zv = valid ? __uint_as_float(vp & 0xffff0000u) : 0.f;
+        const float rsv = __fdividef(1.f, sv);
+        // 4 bits as e4m3: every other token holds 15 - n and meets -w
+        const float zc = fmaf(zv, rsv, E4 ? (t & 1 ? 15.f : 0.f) : kMid);
+        uint8_t* const at = dyn + L::kOffT + buf * (128 * 24);
+        reinterpret_cast<float4*>(at)[t] = make_float4(p.scale_log2 * sk, p.scale_log2 * fmaf(kMid, sk, zk), __log2f(sv), rsv);
+        reinterpret_cast<float2*>(at + 128 * 16)[t] =
+            make_float2(zc, __int_as_float(valid ? pos - (Lb - p.R) - p.r0 : kHidden));
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(BAR(b_ready + buf));
+        mbar_arrive(BAR(B_UF + buf));
         mbar_arrive(BAR(B_EMPTY + st));
       }
     }
@@ -675,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     const uint32_t sign = E4 && (t & 1) ? 0x80008000u : 0u;   // every other token's weights are negated
 
     // barriers of a stage's products: S^T(x) complete; O^T with x's part complete
-    auto s_done = [&](int x) { return mbar_wait(BAR(B_KE + x % NB), (x / NB) & 1, &s_abort, p.status); };
+    auto s_done = [&](int x) { return mbar_wait(BAR(B_KE + x % NKE), (x / NKE) & 1, &s_abort, p.status); };
     auto o_done = [&](int x) { return mbar_wait(BAR(B_VE + x % NB), (x / NB) & 1, &s_abort, p.status); };
     constexpr int C = NR <= 8 ? NR : 8;                  // rows read from TMEM at once
     auto tm_load = [&](uint32_t at, float* x) {
@@ -702,7 +749,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         q_prefetch(nx);
       }
       const int nst = (sg.npg + ppt - 1) / ppt;
-      const int Lb = p.context_lens[sg.b];
       if (t < NR) s_nu[wg][t] = kNuInit;
       float l[NR], corr[NR];
 #pragma unroll
@@ -715,44 +761,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       const int g0 = g;
       for (; g < g0 + nst; ++g) {
         if (ALT && (g & 1) != wg) continue;
-        const int st = g % NS, sb = g & 1;
-        ok &= mbar_wait(BAR(B_FULL + st), (g / NS) & 1, &s_abort, p.status);
-        // this thread's token: parameters, position, hidden rows
-        const uint8_t* pg = sKV + st * L::kStage + (t / P) * Y.page_bytes;
-        const uint32_t kp = *reinterpret_cast<const uint32_t*>(pg + Y.off_kp + (t % P) * 4);
-        const uint32_t vp = *reinterpret_cast<const uint32_t*>(pg + Y.off_vp + (t % P) * 4);
-        const int lp = s_stage_lp[st][t / P];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_EMPTY + st));
-        const int pos = lp * P + (t % P);
-        const bool valid = lp >= 0 && pos < Lb;
-        uint32_t hide = valid ? 0u : ~0u;
-        const int excess = pos - (Lb - p.R) - p.r0;      // rows before it do not see the token
-        if (valid && excess > 0) {
+        const int sb = g & 1;
+        ok &= mbar_wait(BAR(B_UF + g % NB), (g / NB) & 1, &s_abort, p.status);
+        const uint8_t* const tp = dyn + L::kOffT + (g % NB) * (128 * 24);
+        const float4 ta = reinterpret_cast<const float4*>(tp)[t];
+        const float2 tb = reinterpret_cast<const float2*>(tp + 128 * 16)[t];
+        const float ka = ta.x, kb = ta.y;
+        float lgs = ta.z, rsv = ta.w, zc = tb.x;
+        const int excess = __float_as_int(tb.y);
+        uint32_t hide = 0u;
+        if (excess > 0) {
           const int nm = p.G * excess - rb;
-          hide = nm <= 0 ? 0u : nm >= 32 ? ~0u : (1u << nm) - 1u;
+          hide = excess == kHidden || nm >= 32 ? ~0u : nm <= 0 ? 0u : (1u << nm) - 1u;
         }
-        const float sk = __uint_as_float(kp << 16), zk = __uint_as_float(kp & 0xffff0000u);
-        float sv = __uint_as_float(vp << 16);
-        float zc = __fdividef(__uint_as_float(vp & 0xffff0000u), sv) + (E4 ? (t & 1 ? 15.f : 0.f) : kMid);
-        const float ka = p.scale_log2 * sk, kb = p.scale_log2 * fmaf(kMid, sk, zk);
-        if (!valid) {
-          sv = 1.f;
-          zc = 0.f;
-        } else if (!(fabsf(sv) + fabsf(zc) < INFINITY)) {   // a NaN row: the rows that see it, and only they
+        if (!(fabsf(zc) + rsv < INFINITY)) {             // a NaN row of values: the rows that see it, and only they
 #pragma unroll
           for (int r = 0; r < NR; ++r)
             if (!((hide >> r) & 1u)) corr[r] = __int_as_float(0x7fc00000);
-          sv = 1.f;
-          zc = 0.f;
+          lgs = zc = 0.f;
+          rsv = 1.f;
         }
-        const float rsv = __fdividef(1.f, sv), lgs = __log2f(sv);
         ok &= s_done(g);
         tc_fence_after();
         float s[NR];
         // s <- y + log2 s_v (- reference); hidden: -inf
         auto load_s = [&](bool with_ref) {
-          const uint32_t at = tmem + lane_base + L::kColS + sb * N + rb;
+          const uint32_t at = tmem + lane_base + L::kColS + g % NSB * N + rb;
           if constexpr (E4) {
             float lo[NR];
             if constexpr (NR == 4) {
@@ -863,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_PF + sb));
+        if (lane == 0) mbar_arrive(BAR(B_PF + g % NSB));
         mine = g;
       }
       if (abort_all) break;
