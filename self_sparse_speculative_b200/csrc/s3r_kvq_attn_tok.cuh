@@ -77,7 +77,7 @@ struct Lay {
   static constexpr int kKCols = kTile * D / 128;           // of a stage's keys
   static constexpr uint32_t kRowK = E4 ? 128 : 64;         // of k in one 128-byte row of Q and w
   static constexpr uint32_t kQBytes = N * 128 * ((D + kRowK - 1) / kRowK);   // [blocks of kRowK][N rows][128 B], two (segment parity)
-  static constexpr uint32_t kPBytes = N * 128 * (kTok / kRowK);              // two (stage parity)
+  static constexpr uint32_t kPBytes = E4 ? N * kTok : kTok * 128;   // E4: [N rows][128 B of k], f16: [128 k][up to 64 rows], two (stage parity)
   static constexpr uint32_t kXBytes = ALT ? NR * 128 * 4 : 0;   // O^T of the second warpgroup, [row][channel]
   static constexpr uint32_t kStage = 2 * (kTok * D * BITS / 8) + 8 * kTok;
   static constexpr uint32_t kOffP = 2 * kQBytes;
@@ -85,11 +85,13 @@ struct Lay {
   // TMEM columns: NB key tiles, NB value tiles, S^T[NSB], O^T[1 or 2]
   static constexpr int kO = ALT ? 2 : 1;
   static constexpr int NSB = 4 * kTile + (4 + kO) * N <= 512 ? 4 : 2;
-  static constexpr int NB = 8 * kTile + (NSB + kO) * N <= 512 ? 4 : 2;
+  static constexpr int kFit = (512 - (NSB + kO) * N) / (2 * kTile);
+  static constexpr int NB = kFit >= 4 ? 4 : 2;
+  static constexpr int kNT = E4 ? NB : NB + NSB <= 4 ? 4 : 8;   // stages of tokens' parameters
   static constexpr int NKE = NB > NSB ? NB : NSB;          // products of keys whose completion may still be waited for
   static constexpr uint32_t kColK = 0, kColV = kTile * NB, kColS = 2 * kTile * NB, kColO = kColS + NSB * N;
-  static constexpr uint32_t kOffT = kOffX + kXBytes;       // tokens' parameters, NB stages: float4 [128], float2 [128]
-  static constexpr uint32_t kOffKV = kOffT + NB * 128 * 24;
+  static constexpr uint32_t kOffT = kOffX + kXBytes;       // tokens' parameters: float4 [128], float2 [128] a stage
+  static constexpr uint32_t kOffKV = kOffT + kNT * 128 * 24;
   static constexpr int kNSraw = (kSmemBudget - (int)kOffKV - 1024) / (int)kStage;
   static constexpr int kNS = kNSraw >= 8 ? 8 : kNSraw >= 4 ? 4 : 2;   // ring sizes are powers of two
   static constexpr uint32_t kDynBytes = kOffKV + kNS * kStage + 1024;
@@ -97,7 +99,8 @@ struct Lay {
   // slack before it is raised again: weights stay below 256 or 2^15
   static constexpr float kTop = E4 ? 6.f : 8.f, kTau = E4 ? 2.f : 7.f;
   static_assert(kNSraw >= 2, "the ring needs two stages");
-  static_assert(2 * kTile * NB + (NSB + kO) * N <= 512, "TMEM columns");
+  static_assert(NB >= 2 && 2 * kTile * NB + (NSB + kO) * N <= 512, "TMEM columns");
+  static_assert(E4 || kNT >= NB + NSB, "a token's parameters outlive the stages in flight");
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, f32 accumulate: 32 of k of e4m3 or 16 of f16.
@@ -167,9 +170,10 @@ __device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void* src, ui
                :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy) : "memory");
 }
 
-// Instruction descriptor, f16 A/B (kind::f16) or e4m3 A/B (kind::f8f6f4), f32 accumulator, both K-major.
-__host__ __device__ constexpr uint32_t idesc_f32(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// Instruction descriptor, f16 A/B (kind::f16) or e4m3 A/B (kind::f8f6f4), f32
+// accumulator, A K-major, B K-major or N-major.
+__host__ __device__ constexpr uint32_t idesc_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 __device__ __forceinline__ uint32_t fma2(uint32_t a, float k, float c) {
@@ -201,6 +205,28 @@ __device__ __forceinline__ void unpack_e4(uint32_t w, uint32_t* r) {
   r[1] = ((w >> 4) ^ (ALT ? ~0u : 0u)) & 0x0f0f0f0fu;
 }
 
+// Two rows at once: d = a b + c, d = a b.
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul_pair(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -227,10 +253,11 @@ __device__ __forceinline__ Split split2(uint32_t h2) {
   s.lo = e4m3x2_of(*reinterpret_cast<const uint32_t*>(&lo));
   return s;
 }
-// x rounded to 9 significant bits.
-__device__ __forceinline__ float round9(float x) {
-  const float c = x * 32769.f;
-  return __fsub_rn(c, __fsub_rn(c, x));
+// Rounded to 9 significant bits.
+__device__ __forceinline__ float2 round9(float2 x) {
+  const float2 c = mul_pair(x, both(32769.f));
+  const float2 d = fma_pair(x, both(-1.f), c);             // c - x
+  return fma_pair(d, both(-1.f), c);
 }
 
 // Reduce C per-row values over the warp: lane l ends with row l % C.
@@ -283,6 +310,50 @@ __device__ __forceinline__ int count_wg(int wg, bool pred) {
   return r;
 }
 
+// A value that all lanes hold, as one the compiler knows to be uniform: role,
+// loop and address arithmetic then run once a warp (without it the 8-bit
+// case of 16 x 16384 tokens and 5 rows took 180 us instead of 140).
+__device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ Seg locate_uni(const KvqAttnParams& p, const int* s_prefix, int x, int hi, int W) {
+  Seg s = locate(p, s_prefix, x, hi, W);
+  s.b = (int)uni(s.b);
+  s.h = (int)uni(s.h);
+  s.k0 = (int)uni(s.k0);
+  s.npg = (int)uni(s.npg);
+  s.end = (int)uni(s.end);
+  s.unit = (int)uni(s.unit);
+  s.first_cta = (int)uni(s.first_cta);
+  s.nseg = (int)uni(s.nseg);
+  return s;
+}
+// Stages of a CTA's range in order: g of all, j of the nst of segment s.
+struct Walk {
+  Seg sg;
+  int s, j, nst;
+  uint32_t g;
+  bool valid;
+};
+__device__ __forceinline__ Walk walk_begin(const KvqAttnParams& p, const int* s_prefix, int lo, int hi, int W, int ppt) {
+  Walk w;
+  w.s = w.j = 0;
+  w.g = 0u;
+  w.valid = lo < hi;
+  w.sg = locate_uni(p, s_prefix, lo, hi, W);
+  w.nst = (w.sg.npg + ppt - 1) / ppt;
+  return w;
+}
+__device__ __forceinline__ void walk_next(const KvqAttnParams& p, const int* s_prefix, int hi, int W, int ppt, Walk& w) {
+  ++w.g;
+  if (++w.j < w.nst) return;
+  w.j = 0;
+  ++w.s;
+  w.valid = w.sg.end < hi;
+  if (w.valid) {
+    w.sg = locate_uni(p, s_prefix, w.sg.end, hi, W);
+    w.nst = (w.sg.npg + ppt - 1) / ppt;
+  }
+}
+
 // Listed pages are all walked, -1 entries among them.
 __device__ __forceinline__ int unit_pages(const KvqAttnParams& p, int L) {
   if (kvq_bad_context(p, L)) return 0;
@@ -294,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   using L = Lay<NR, ALT, D, BITS>;
   constexpr KvqLayout Y = kvq_layout(D, P, BITS);
   constexpr int kUnit = Y.unit;                          // bytes of a V piece
-  constexpr int NRT = L::NRT, N = L::N, NB = L::NB, NS = L::kNS, NSB = L::NSB, NKE = L::NKE;
+  constexpr int NRT = L::NRT, N = L::N, NB = L::NB, NS = L::kNS, NSB = L::NSB, NKE = L::NKE, kNT = L::kNT;
   constexpr int ppt = kTok / P;                          // pages per stage
   constexpr bool E4 = L::E4;
   constexpr float kTop = L::kTop, kTau = L::kTau;
@@ -302,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   static_assert(ppt * Y.page_bytes == (int)L::kStage, "stage bytes");
   extern __shared__ __align__(1024) uint8_t dyn_raw[];
   uint8_t* dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t s_bar[2 * NS + 2 * NB + NKE + NSB + 4];
+  __shared__ __align__(8) uint64_t s_bar[2 * NS + 3 * NB + NKE + kNT + NSB + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_ticket;
@@ -324,7 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   __shared__ __align__(16) float s_qs[2][64];            // by segment parity: sum of a query row
   __shared__ __align__(16) float s_qf[2][64];            // 1 / the query row's scale
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = (int)uni((uint32_t)tid >> 5);
   pdl_launch_dependents();
 
   if (warp == 0) {                                       // per-sequence prefix of unit pages
@@ -357,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       for (int h = 0; h < p.Hkv; ++h) kvq_write_empty<__nv_bfloat16>(p, b, h, tid, kThreads);
     }
   }
-  const int total = s_prefix[p.S];
+  const int total = (int)uni((uint32_t)s_prefix[p.S]);
   // at least one stage of pages per CTA (shorter pieces would cost a merge
   // for less than a stage); with lists, a whole unit per CTA where the units
   // nearly fill the grid, so that none is split
@@ -371,13 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
 
   const uint32_t bar0 = smem_addr(&s_bar[0]);
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-  // UF: a stage is unpacked (both tiles in TMEM, token parameters in shared
-  // memory); KE / VE: its product of keys / values is done (S^T / O^T has its
-  // part; VE: tiles and parameters are free); PF: w(g) is written (and S^T(g)
-  // and the parameters read). Stage g uses barrier g % size of each ring, and each
-  // ring is as long as the stages between a completion and its last waiter, so
-  // that none is two phases ahead of a wait.
-  constexpr int B_FULL = 0, B_EMPTY = NS, B_UF = 2 * NS, B_KE = B_UF + NB, B_VE = B_KE + NKE,
+  // KF / VF: a stage's keys / values are unpacked in TMEM; TF: its token
+  // parameters are in shared memory; KE / VE: its product of keys / values is
+  // done (S^T / O^T has its part, the tile is free); PF: w(g) is written (and
+  // S^T(g) and the parameters read). Stage g uses barrier g % size of each
+  // ring, and each ring is as long as the stages between a completion and its
+  // last waiter, so that none is two phases ahead of a wait.
+  constexpr int B_FULL = 0, B_EMPTY = NS, B_KF = 2 * NS, B_VF = B_KF + NB, B_TF = B_VF + NB, B_KE = B_TF + kNT, B_VE = B_KE + NKE,
                 B_PF = B_VE + NB, B_QF = B_PF + NSB, B_TD = B_QF + 1, B_X = B_TD + 1, B_Y = B_X + 1;
   uint8_t* sQ = dyn;
   uint8_t* sP = dyn + L::kOffP;
@@ -391,13 +463,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(BAR(B_FULL + i), 1);
-      mbar_init(BAR(B_EMPTY + i), 4);                    // the warps that unpack the stage
+      mbar_init(BAR(B_EMPTY + i), E4 ? 4 : 8);           // the warps that unpack the stage
     }
     for (int i = 0; i < NB; ++i) {
-      mbar_init(BAR(B_UF + i), 4);
+      mbar_init(BAR(B_KF + i), 4);
+      mbar_init(BAR(B_VF + i), 4);
       mbar_init(BAR(B_VE + i), 1);
     }
     for (int i = 0; i < NKE; ++i) mbar_init(BAR(B_KE + i), 1);
+    for (int i = 0; i < kNT; ++i) mbar_init(BAR(B_TF + i), 4);
     for (int i = 0; i < NSB; ++i) mbar_init(BAR(B_PF + i), ALT ? 4 : 8);
     mbar_init(BAR(B_QF), 8);
     mbar_init(BAR(B_TD), 2);
@@ -410,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = uni(s_tmem);
 
   if (warp == kProducer) {
     // ======================================================= producer warp
@@ -427,8 +501,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       if (there) *ph = p.block_table[(size_t)s.b * p.max_pages + *lp];
     };
     bool waited = p.page_list != nullptr, ok = true, more = true;
-    int g = 0, k = 0, lp, ph;
-    Seg sg = locate(p, s_prefix, lo, hi, W);
+    uint32_t g = 0;
+    int k = 0, lp, ph;
+    Seg sg = locate_uni(p, s_prefix, lo, hi, W);
     look_up(sg, 0, &lp, &ph);
     while (more && ok) {
       Seg nx = sg;
@@ -436,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       if (nk >= sg.npg) {
         nk = 0;
         more = sg.end < hi;
-        if (more) nx = locate(p, s_prefix, sg.end, hi, W);
+        if (more) nx = locate_uni(p, s_prefix, sg.end, hi, W);
       }
       if (more) look_up(nx, nk, &nlp, &nph);
       if (lp != -1 && (ph < 0 || ph >= p.num_pages_total)) {
@@ -447,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       const int stages = (min(32, sg.npg - k) + ppt - 1) / ppt;
       const uint8_t* const src = p.pages + ((size_t)max(ph, 0) * p.Hkv + sg.h) * Y.page_bytes;
       for (int j = 0; j < stages; ++j, ++g) {
-        const int st = g % NS;
+        const uint32_t st = g % NS;
         if (g == NS && !waited) {                        // the ring's first fill goes out before it
           pdl_wait();
           waited = true;
@@ -473,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     if (!waited) pdl_wait();
     // drain: wait until every issued copy has landed
     if (lane == 0)
-      for (int k = max(0, g - NS); k < g; ++k) mbar_wait_drain(BAR(B_FULL + k % NS), (k / NS) & 1, p.status);
+      for (uint32_t k = g > NS ? g - NS : 0; k < g; ++k) mbar_wait_drain(BAR(B_FULL + k % NS), (k / NS) & 1, p.status);
   } else if (warp >= kMmaQk) {
     // ======================================================= MMA issuers
     // One warp for each product, in stage order. The whole warp runs the loop
@@ -483,42 +558,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     // both the unpacking warps (tile free) and the softmax (product done) wait on.
     // QK(g) needs its stage unpacked, w(g - NSB) written (S^T buffer g % NSB has been read)
     // and first in a segment the segment's Q; PV(g) needs w(g).
-    constexpr uint32_t idesc = idesc_f32(128, N);
-    auto uni = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
-    const uint32_t tm = uni(tmem);
-    // Q and w: K-major, 128-byte rows, 8-row groups 1024 B apart; a step of
-    // k is 32 bytes inside the swizzle row, the next row N x 128 B further.
-    // A tile's step is 8 TMEM columns.
+    constexpr uint32_t idQk = idesc_f32(128, N, false), idPv = idesc_f32(128, N, !E4);
+    // Q (and w of E4): K-major, 128-byte rows, 8-row groups 1024 B apart; a
+    // step of k is 32 bytes inside the swizzle row, the next row N x 128 B
+    // further. w in f16: rows along the 128 bytes, a step of k 16 tokens, 2048
+    // B. A tile's step is 8 TMEM columns.
     const uint64_t dB0 = smem_desc_sw128(warp == kMmaQk ? aQ : aP, 16, 1024);
     constexpr uint32_t kBlock = (N * 128) >> 4;
-    for (Cursor c = cursor_begin(p, s_prefix, lo, hi, W, ppt); uni(c.valid); cursor_next(p, s_prefix, hi, W, ppt, c)) {
-      const int buf = c.g % NB;
+    for (Walk c = walk_begin(p, s_prefix, lo, hi, W, ppt); c.valid; walk_next(p, s_prefix, hi, W, ppt, c)) {
+      const uint32_t buf = c.g % NB;
       if (warp == kMmaQk) {
-        bool ok = mbar_wait(BAR(B_UF + buf), (c.g / NB) & 1, &s_abort, p.status);
+        bool ok = mbar_wait(BAR(B_KF + buf), (c.g / NB) & 1, &s_abort, p.status);
         if (c.g >= NSB) ok = ok && mbar_wait(BAR(B_PF + c.g % NSB), (c.g / NSB - 1) & 1, &s_abort, p.status);
         if (c.j == 0) ok = ok && mbar_wait(BAR(B_QF), c.s & 1, &s_abort, p.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const uint32_t d = uni(tm + L::kColS + c.g % NSB * N), a = uni(tm + L::kColK + buf * L::kTile);
+        const uint32_t d = uni(tmem + L::kColS + c.g % NSB * N), a = uni(tmem + L::kColK + buf * L::kTile);
         const uint32_t bar = uni(BAR(B_KE + c.g % NKE)), step = uni((c.s & 1) * (L::kQBytes >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < L::kKCols / 8; ++kk)
-            umma_ta<E4>(d, a + kk * 8, dB0 + step + (kk >> 2) * kBlock + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
+            umma_ta<E4>(d, a + kk * 8, dB0 + step + (kk >> 2) * kBlock + (kk & 3) * 2, idQk, kk > 0 ? 1u : 0u);
           umma_commit(bar);
         }
       } else {
-        bool ok = mbar_wait(BAR(B_UF + buf), (c.g / NB) & 1, &s_abort, p.status);
+        bool ok = mbar_wait(BAR(B_VF + buf), (c.g / NB) & 1, &s_abort, p.status);
         ok = ok && mbar_wait(BAR(B_PF + c.g % NSB), (c.g / NSB) & 1, &s_abort, p.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const uint32_t d = uni(tm + L::kColO + (ALT ? (c.g & 1) * N : 0)), a = uni(tm + L::kColV + buf * L::kTile);
+        const uint32_t d = uni(tmem + L::kColO + (ALT ? (c.g & 1) * N : 0)), a = uni(tmem + L::kColV + buf * L::kTile);
         const uint32_t first = uni(c.j >= (ALT ? 2 : 1) ? 1u : 0u), bar = uni(BAR(B_VE + buf));
         const uint32_t step = uni((c.g & 1) * (L::kPBytes >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < L::kTile / 8; ++kk)
-            umma_ta<E4>(d, a + kk * 8, dB0 + step + (kk >> 2) * kBlock + (kk & 3) * 2, idesc, kk > 0 ? 1u : first);
+            umma_ta<E4>(d, a + kk * 8, dB0 + step + kk * (E4 ? 2 : 2048 >> 4), idPv, kk > 0 ? 1u : first);
           umma_commit(bar);
         }
       }
@@ -528,31 +602,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     __syncwarp();
   } else if (warp >= 8) {
     // ======================================================= unpacking warps
-    // The warpgroups take alternate stages, keys and values, so that a
-    // warpgroup's chain of waits, loads and stores spans two stages. The tiles
+    // E4: the warpgroups take alternate stages, keys and values, so that a
+    // warpgroup's chain of waits, loads and stores spans two stages; the tiles
     // and parameters of stage g - NB are free once its product of values is
-    // done: its product of keys and its softmax came before.
+    // done. Else (two or three tiles in TMEM): one takes the keys and
+    // parameters, one the values, so that keys run ahead of the softmax (5 rows
+    // of 16 x 16384 tokens in 8 bits: 146 us, alternating 160).
     split_registers<false>();
     const int uwg = (warp - 8) >> 2;
     const int t = tid & 127;                             // TMEM lane: token of S^T, channel of O^T
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
     constexpr int kWordsPage = P * BITS / 32;            // words of a channel in one page: 2, 4, 8 or 16
     constexpr int kHalfWords = 64 * BITS / 32;           // f16: words of 32 columns' numbers, 8 or 16
-    Cursor c = cursor_begin(p, s_prefix, lo, hi, W, ppt);
     int Lb = -1, of = -1;                                // length of sequence `of`
-    for (; c.valid; cursor_next(p, s_prefix, hi, W, ppt, c)) {
-      const uint32_t g = (uint32_t)c.g, st = g % NS, buf = g % NB;
-      if ((g & 1u) != (uint32_t)uwg) continue;
+    for (Walk c = walk_begin(p, s_prefix, lo, hi, W, ppt); c.valid; walk_next(p, s_prefix, hi, W, ppt, c)) {
+      const uint32_t g = c.g, st = g % NS, buf = g % NB;
+      if (E4 && (g & 1u) != (uint32_t)uwg) continue;
       if (of != c.sg.b) {
         of = c.sg.b;
         Lb = p.context_lens[of];
       }
       bool ok = mbar_wait(BAR(B_FULL + st), (g / NS) & 1, &s_abort, p.status);
-      if (g >= NB) ok = ok && mbar_wait(BAR(B_VE + buf), (g / NB - 1) & 1, &s_abort, p.status);
+      if (g >= NB) {
+        const uint32_t x = g - NB;
+        ok = ok && (E4 || uwg == 1 ? mbar_wait(BAR(B_VE + buf), (x / NB) & 1, &s_abort, p.status)
+                                   : mbar_wait(BAR(B_KE + x % NKE), (x / NKE) & 1, &s_abort, p.status));
+      }
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint8_t* const stage = sKV + st * L::kStage;
-      {
+      if (E4 || uwg == 0) {
         const uint32_t dst = tmem + lane_base + L::kColK + buf * L::kTile;
         const uint8_t* const row = stage + (t / P) * Y.page_bytes + (t % P) * 16;
         auto words = [&](int k) { return *reinterpret_cast<const uint4*>(row + (k / 4) * (P * 16)); };
@@ -582,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           else tmem_st16_raw(dst, r);
         }
       }
-      if (D == 128 || t < D) {                           // whole warps; lanes past D hold anything and are never read
+      if ((E4 || uwg == 1) && (D == 128 || t < D)) {     // whole warps; lanes past D hold anything and are never read
         const uint32_t dst = tmem + lane_base + L::kColV + buf * L::kTile;
         auto words = [&](int k) {
           const int pg = k / kWordsPage;
@@ -620,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       // the token's parameters for the softmax: y = ka S^T + kb sum q (scaled),
       // log2 s_v, 1 / s_v, the centre of its values over s_v, and its position
       // against the rows' (hidden from rows before `excess`; from all: kHidden)
-      {
+      if (E4 || uwg == 0) {
         const uint8_t* pg = stage + (t / P) * Y.page_bytes;
         const uint32_t kp = *reinterpret_cast<const uint32_t*>(pg + Y.off_kp + (t % P) * 4);
         const uint32_t vp = *reinterpret_cast<const uint32_t*>(pg + Y.off_vp + (t % P) * 4);
@@ -633,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         const float rsv = __fdividef(1.f, sv);
         // 4 bits as e4m3: every other token holds 15 - n and meets -w
         const float zc = fmaf(zv, rsv, E4 ? (t & 1 ? 15.f : 0.f) : kMid);
-        uint8_t* const at = dyn + L::kOffT + buf * (128 * 24);
+        uint8_t* const at = dyn + L::kOffT + (g % kNT) * (128 * 24);
         reinterpret_cast<float4*>(at)[t] = make_float4(p.scale_log2 * sk, p.scale_log2 * fmaf(kMid, sk, zk), __log2f(sv), rsv);
         reinterpret_cast<float2*>(at + 128 * 16)[t] =
             make_float2(zc, __int_as_float(valid ? pos - (Lb - p.R) - p.r0 : kHidden));
@@ -642,7 +721,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(BAR(B_UF + buf));
+        if (E4 || uwg == 0) {
+          mbar_arrive(BAR(B_KF + buf));
+          mbar_arrive(BAR(B_TF + g % kNT));
+        }
+        if (E4 || uwg == 1) mbar_arrive(BAR(B_VF + buf));
         mbar_arrive(BAR(B_EMPTY + st));
       }
     }
@@ -717,13 +800,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     };
     // where this thread's weights go: its token's place along k
     const int kpos = E4 ? (t & ~7) + ((t & 1) << 2) + ((t & 7) >> 1) : BITS == 4 ? (t & ~7) + ((t & 3) << 1) + ((t >> 2) & 1) : t;
-    uint8_t* const pw = E4 ? sP + (kpos & 15) : sP + (kpos >> 6) * (N * 128) + rb * 128 + (kpos & 7) * 2;
-    const int pck = E4 ? kpos >> 4 : (kpos & 63) >> 3;
+    uint8_t* const pw = E4 ? sP + (kpos & 15) : sP + kpos * 128;
+    const int pck = E4 ? kpos >> 4 : kpos & 7;
     const uint32_t sign = E4 && (t & 1) ? 0x80008000u : 0u;   // every other token's weights are negated
 
     // barriers of a stage's products: S^T(x) complete; O^T with x's part complete
-    auto s_done = [&](int x) { return mbar_wait(BAR(B_KE + x % NKE), (x / NKE) & 1, &s_abort, p.status); };
-    auto o_done = [&](int x) { return mbar_wait(BAR(B_VE + x % NB), (x / NB) & 1, &s_abort, p.status); };
+    auto s_done = [&](uint32_t x) { return mbar_wait(BAR(B_KE + x % NKE), (x / NKE) & 1, &s_abort, p.status); };
+    auto o_done = [&](uint32_t x) { return mbar_wait(BAR(B_VE + x % NB), (x / NB) & 1, &s_abort, p.status); };
     constexpr int C = NR <= 8 ? NR : 8;                  // rows read from TMEM at once
     auto tm_load = [&](uint32_t at, float* x) {
       if constexpr (C == 4) tmem_ld4(at, x);
@@ -734,18 +817,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       if constexpr (C == 4) tmem_st4(at, x);
       else tmem_st8(at, x);
     };
-    Seg sg = locate(p, s_prefix, lo, hi, W);
+    Seg sg = locate_uni(p, s_prefix, lo, hi, W);
     q_prefetch(sg);                                      // an input: no earlier kernel writes it
     pdl_wait();
     q_store(sg, 0);
-    int g = 0, seg = 0;
+    uint32_t g = 0;
+    int seg = 0;
     bool ok = true;
     for (int x = lo; x < hi; ++seg) {
       const int par = seg & 1;
       const bool has_next = sg.end < hi;
       Seg nx = sg;
       if (has_next) {
-        nx = locate(p, s_prefix, sg.end, hi, W);
+        nx = locate_uni(p, s_prefix, sg.end, hi, W);
         q_prefetch(nx);
       }
       const int nst = (sg.npg + ppt - 1) / ppt;
@@ -758,12 +842,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       ok &= mbar_wait(BAR(B_QF), par, &s_abort, p.status);
       bool abort_all = false;
       int mine = -1;                                     // this warpgroup's last stage of the segment
-      const int g0 = g;
+      const uint32_t g0 = g;
       for (; g < g0 + nst; ++g) {
-        if (ALT && (g & 1) != wg) continue;
-        const int sb = g & 1;
-        ok &= mbar_wait(BAR(B_UF + g % NB), (g / NB) & 1, &s_abort, p.status);
-        const uint8_t* const tp = dyn + L::kOffT + (g % NB) * (128 * 24);
+        if (ALT && (int)(g & 1) != wg) continue;
+        const uint32_t sb = g & 1;
+        ok &= mbar_wait(BAR(B_TF + g % kNT), (g / kNT) & 1, &s_abort, p.status);
+        const uint8_t* const tp = dyn + L::kOffT + (g % kNT) * (128 * 24);
         const float4 ta = reinterpret_cast<const float4*>(tp)[t];
         const float2 tb = reinterpret_cast<const float2*>(tp + 128 * 16)[t];
         const float ka = ta.x, kb = ta.y;
@@ -798,7 +882,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
             }
             tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < NR; ++r) s[r] = fmaf(lo[r], kLo, s[r]);
+            for (int r = 0; r < NR; r += 2) {
+              const float2 v = fma_pair(make_float2(lo[r], lo[r + 1]), both(kLo), make_float2(s[r], s[r + 1]));
+              s[r] = v.x;
+              s[r + 1] = v.y;
+            }
           } else {
             if constexpr (NR == 4) tmem_ld4(at, s);
             else tmem_ld_cols<NR>(at, s);
@@ -810,10 +898,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
             const float4 qf = *reinterpret_cast<const float4*>(&s_qf[par][rb + r]);
             float4 nu = make_float4(0.f, 0.f, 0.f, 0.f);
             if (with_ref) nu = *reinterpret_cast<const float4*>(&s_nu[wg][r]);
-            s[r] = fmaf(s[r] * qf.x, ka, fmaf(qs.x, kb, nu.x + lgs));
-            s[r + 1] = fmaf(s[r + 1] * qf.y, ka, fmaf(qs.y, kb, nu.y + lgs));
-            s[r + 2] = fmaf(s[r + 2] * qf.z, ka, fmaf(qs.z, kb, nu.z + lgs));
-            s[r + 3] = fmaf(s[r + 3] * qf.w, ka, fmaf(qs.w, kb, nu.w + lgs));
+            auto y = [&](float2 x, float2 f, float2 q, float2 n) {
+              return fma_pair(mul_pair(x, f), both(ka), fma_pair(q, both(kb), fma_pair(n, both(1.f), both(lgs))));
+            };
+            const float2 a = y(make_float2(s[r], s[r + 1]), make_float2(qf.x, qf.y), make_float2(qs.x, qs.y), make_float2(nu.x, nu.y));
+            const float2 b = y(make_float2(s[r + 2], s[r + 3]), make_float2(qf.z, qf.w), make_float2(qs.z, qs.w),
+                               make_float2(nu.z, nu.w));
+            s[r] = a.x;
+            s[r + 1] = a.y;
+            s[r + 2] = b.x;
+            s[r + 3] = b.y;
           }
           if (hide) {
 #pragma unroll
@@ -822,9 +916,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           }
         };
         load_s(true);
-        float ymax = s[0];
+        float ymax = fmaxf(s[0], s[1]);
 #pragma unroll
-        for (int r = 1; r < NR; ++r) ymax = fmaxf(ymax, s[r]);
+        for (int r = 2; r < NR; r += 2) ymax = max3(ymax, s[r], s[r + 1]);
         // one barrier per stage: stop together, or raise the references together
         const int cnt = count_wg(wg, !ok || ymax > kTop + kTau);
         bool rescale_o = false;
@@ -854,8 +948,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         }
         // w buffer sb was last read by PV(g - 2); a rescale of O^T also needs
         // its last PV done (ALT: the same)
-        const int gw = g - (!ALT && rescale_o ? 1 : 2);
-        if (gw >= 0) ok &= o_done(gw);
+        const uint32_t back = !ALT && rescale_o ? 1 : 2;
+        if (g >= back) ok &= o_done(g - back);
         tc_fence_after();
         if (rescale_o) {
 #pragma unroll
@@ -870,35 +964,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           tmem_wait_st();
         }
         uint8_t* const pb = pw + sb * L::kPBytes;
+        uint32_t h[NR / 2];
 #pragma unroll
         for (int r = 0; r < NR; r += 2) {
-          float w0 = ex2(s[r]), w1 = ex2(s[r + 1]);
-          l[r] = fmaf(w0, rsv, l[r]);
-          l[r + 1] = fmaf(w1, rsv, l[r + 1]);
+          float2 w = make_float2(ex2(s[r]), ex2(s[r + 1]));
+          const float2 ln = fma_pair(w, both(rsv), make_float2(l[r], l[r + 1]));
+          l[r] = ln.x;
+          l[r + 1] = ln.y;
+          if constexpr (E4) w = round9(w);               // the numbers' and the minima's sums meet the same rounded weight
+          const float2 cn = fma_pair(w, both(zc), make_float2(corr[r], corr[r + 1]));
+          corr[r] = cn.x;
+          corr[r + 1] = cn.y;
+          h[r / 2] = half2_of(w.x, w.y);
           if constexpr (E4) {
-            // the numbers' and the minima's sums meet the same rounded weight
-            w0 = round9(w0);
-            w1 = round9(w1);
-          }
-          corr[r] = fmaf(w0, zc, corr[r]);
-          corr[r + 1] = fmaf(w1, zc, corr[r + 1]);
-          const uint32_t h = half2_of(w0, w1);
-          if constexpr (E4) {
-            const Split sp = split2(h ^ sign);
+            const Split sp = split2(h[r / 2] ^ sign);
             pb[r * 128 + ((pck ^ (r & 7)) << 4)] = (uint8_t)sp.hi;
             pb[(r + 1) * 128 + ((pck ^ ((r + 1) & 7)) << 4)] = (uint8_t)(sp.hi >> 8);
             pb[(NRT + r) * 128 + ((pck ^ ((NRT + r) & 7)) << 4)] = (uint8_t)sp.lo;
             pb[(NRT + r + 1) * 128 + ((pck ^ ((NRT + r + 1) & 7)) << 4)] = (uint8_t)(sp.lo >> 8);
+          }
+        }
+        if constexpr (!E4) {
+          // eight rows of this token are 16 bytes of its row of k
+          if constexpr (NR == 4) {
+            *reinterpret_cast<uint2*>(pb + (pck << 4)) = make_uint2(h[0], h[1]);
           } else {
-            *reinterpret_cast<uint16_t*>(pb + r * 128 + ((pck ^ (r & 7)) << 4)) = (uint16_t)h;
-            *reinterpret_cast<uint16_t*>(pb + (r + 1) * 128 + ((pck ^ ((r + 1) & 7)) << 4)) = (uint16_t)(h >> 16);
+#pragma unroll
+            for (int r = 0; r < NR; r += 8)
+              *reinterpret_cast<uint4*>(pb + (((rb + r) / 8 ^ pck) << 4)) = make_uint4(h[r / 2], h[r / 2 + 1], h[r / 2 + 2], h[r / 2 + 3]);
           }
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_PF + g % NSB));
-        mine = g;
+        mine = (int)g;
       }
       if (abort_all) break;
       // ---- the next segment's Q goes to the other buffer: the products of
@@ -916,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         s_sum[wg][t] = (a[0][t] + a[1][t]) + (a[2][t] + a[3][t]);
         s_corr[wg][t] = (c[0][t] + c[1][t]) + (c[2][t] + c[3][t]);
       }
-      if (mine >= 0) ok &= o_done(mine);                 // PV of the last stage
+      if (mine >= 0) ok &= o_done((uint32_t)mine);                 // PV of the last stage
       tc_fence_after();
       sync_wg(wg);
       float* const sX = reinterpret_cast<float*>(dyn + L::kOffX);
