@@ -53,22 +53,72 @@ struct KvqParams {
   uint32_t* tickets;          // [S]
 };
 
-// 8 consecutive channels of a row as floats.
-template <typename T> __device__ __forceinline__ void load8(const T* p, float* x);
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
-  const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 8 consecutive channels of a row (of this lane), as loaded.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
   }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ __forceinline__ float2 pair(int i) const {
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcg(reinterpret_cast<const float4*>(p));
+    b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float2 pair(int i) const {
+    return i == 0 ? make_float2(a.x, a.y) : i == 1 ? make_float2(a.z, a.w) : i == 2 ? make_float2(b.x, b.y) : make_float2(b.z, b.w);
+  }
+};
+
+// Minimum and maximum over a row (kLanes lanes), NaN if it holds one. bf16:
+// exact in packed bf16, both in one word {min, -max} across the lanes.
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+template <int kLanes>
+__device__ __forceinline__ void row_range(const Raw8<__nv_bfloat16>& x, float* mn, float* mx) {
+  const uint32_t lo = as_u32(__hmin2_nan(__hmin2_nan(as_bf2(x.w[0]), as_bf2(x.w[1])), __hmin2_nan(as_bf2(x.w[2]), as_bf2(x.w[3]))));
+  const uint32_t hi = as_u32(__hmax2_nan(__hmax2_nan(as_bf2(x.w[0]), as_bf2(x.w[1])), __hmax2_nan(as_bf2(x.w[2]), as_bf2(x.w[3]))));
+  uint32_t m = as_u32(__hmin2_nan(as_bf2(__byte_perm(lo, hi ^ 0x80008000u, 0x5410)), as_bf2(__byte_perm(lo, hi ^ 0x80008000u, 0x7632))));
+#pragma unroll
+  for (int o = kLanes / 2; o >= 1; o >>= 1) m = as_u32(__hmin2_nan(as_bf2(m), as_bf2(__shfl_xor_sync(0xffffffffu, m, o))));
+  *mn = __uint_as_float(m << 16);
+  *mx = __uint_as_float((m & 0xffff0000u) ^ 0x80000000u);
 }
-template <> __device__ __forceinline__ void load8<float>(const float* p, float* x) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+template <int kLanes>
+__device__ __forceinline__ void row_range(const Raw8<float>& x, float* mn, float* mx) {
+  float a = x.a.x, b = x.a.x;
+  const float y[7] = {x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    a = min_nan(a, y[i]);
+    b = max_nan(b, y[i]);
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o >= 1; o >>= 1) {
+    a = min_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+    b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, o));
+  }
+  *mn = a;
+  *mx = b;
 }
+
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 template <typename T> __device__ __forceinline__ void store8(T* p, const float* x);
 template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
@@ -79,34 +129,74 @@ template <> __device__ __forceinline__ void store8<float>(float* p, const float*
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Rows x[k] (the 8 channels of this lane in each of NR rows): parameters (in
-// every lane of the row) and numbers, byte b of code[k] = channel b.
-template <int D, int BITS, int NR>
-__device__ __forceinline__ void quantise_rows(const float (*x)[8], uint32_t (*code)[2], uint32_t* param) {
-  float mn[NR], mx[NR];
+// The numbers of 8 values from float64 quotients (rare: kept out of line, its
+// divisions would crowd the instruction cache).
+template <typename T, int BITS>
+__device__ __noinline__ uint2 quantise8_exact(const Raw8<T> x, float z, float s) {
+  float v[8];
 #pragma unroll
-  for (int k = 0; k < NR; ++k) {
-    mn[k] = mx[k] = x[k][0];
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = x.pair(i).x;
+    v[2 * i + 1] = x.pair(i).y;
+  }
+  uint32_t c[2] = {0u, 0u};
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) c[i >> 2] |= kvq_number_exact<BITS>(v[i], z, s) << (8 * (i & 3));
+  return make_uint2(c[0], c[1]);
+}
+
+// The numbers of this lane's 8 channels, byte i of code = channel i; at 4 bits
+// also as 4 bytes of two. They are those of the exact quotient, ties to even:
+// - bf16: exact ties are common (8-bit values and steps). x - z is exact in
+//   float32 unless the two are more than 2^16 apart (tested: both ways back
+//   must be exact), and the quotient corrected by its remainder is the exact one
+//   rounded: it equals a border m + 1/2 only if the quotient does (it is off a
+//   border by at least 2^-17 of itself otherwise).
+// - float32: t = (x - z) (1 / s) is within 3 u t (u = 2^-24, t at most 2^BITS)
+//   of the exact quotient; nearer than 2^-17 (4 bits) or 2^-14 (8 bits), twice
+//   that, to a border, float64 decides.
+// Differences that overflow fail both tests. s is at most 2^-8 of itself below
+// (max - z) / (2^BITS - 1): n may reach 256 at 8 bits (held to 255), 15 at 4.
+template <typename T, int BITS>
+__device__ __forceinline__ void quantise8(const Raw8<T>& x, float z, float s, float inv, uint32_t* code, uint32_t* packed) {
+  constexpr float kMagic = 12582912.f;                   // 1.5 * 2^23: rounds to the nearest whole, ties to even
+  constexpr bool kBf16 = sizeof(T) == 2;
+  uint32_t b[8], off = 0u;
+  float far = 0.f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      mn[k] = min_nan(mn[k], x[k][i]);
-      mx[k] = max_nan(mx[k], x[k][i]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = x.pair(i);
+    const float2 d = fma_pair(both(-z), both(1.f), v);
+    float2 t = fma_pair(d, both(inv), both(0.f));
+    if (kBf16) {
+      t = fma_pair(fma_pair(t, both(-s), d), both(inv), t);
+      const float2 e = fma_pair(fma_pair(d, both(1.f), both(z)), both(-1.f), v);          // x - (d + z)
+      const float2 g = fma_pair(fma_pair(d, both(-1.f), v), both(1.f), both(-z));         // (x - d) - z
+      off |= __float_as_uint(e.x) | __float_as_uint(g.x);
+      off |= __float_as_uint(e.y) | __float_as_uint(g.y);
     }
+    float2 f = fma_pair(t, both(1.f), both(kMagic));
+    if (!kBf16) {
+      const float2 r = fma_pair(fma_pair(f, both(1.f), both(-kMagic)), both(-1.f), t);
+      far = fmaxf(far, fmaxf(fabsf(r.x), fabsf(r.y)));
+      if (!(fabsf(t.x) + fabsf(t.y) < 4096.f)) far = 1.f;
+    }
+    if (BITS == 8) f = make_float2(fminf(f.x, kMagic + 255.f), fminf(f.y, kMagic + 255.f));
+    b[2 * i] = __float_as_uint(f.x);
+    b[2 * i + 1] = __float_as_uint(f.y);
   }
 #pragma unroll
-  for (int o = D / 16; o >= 1; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < NR; ++k) {
-      mn[k] = min_nan(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], o));
-      mx[k] = max_nan(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
-    }
-#pragma unroll
-  for (int k = 0; k < NR; ++k) {
-    const KvqRow r = kvq_row<BITS>(mn[k], mx[k]);
-    param[k] = pack_bf16x2(r.s, r.z);
-    code[k][0] = code[k][1] = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) code[k][i >> 2] |= kvq_number<BITS>(x[k][i], r) << (8 * (i & 3));
+  for (int q = 0; q < 2; ++q)
+    code[q] = __byte_perm(__byte_perm(b[4 * q], b[4 * q + 1], 0x0040), __byte_perm(b[4 * q + 2], b[4 * q + 3], 0x0040), 0x5410);
+  if (kBf16 ? off != 0u : far > 0.5f - (BITS == 4 ? 0x1p-17f : 0x1p-14f)) {
+    const uint2 c = quantise8_exact<T, BITS>(x, z, s);
+    code[0] = c.x;
+    code[1] = c.y;
+  }
+  if (inv == 0.f) code[0] = code[1] = 0u;                // equal values, or a row with NaN or infinity
+  if (BITS == 4) {
+    const uint32_t lo = code[0] | (code[0] >> 4), hi = code[1] | (code[1] >> 4);   // two half-bytes a byte, at bytes 0 and 2
+    *packed = __byte_perm(lo, hi, 0x6420);
   }
 }
 
@@ -144,7 +234,8 @@ __global__ void __launch_bounds__(kKvqThreads) kvq_store_kernel(const KvqParams 
   constexpr int TT = P == 64 ? 32 : 16;                  // tokens per tile
   constexpr int kLanes = D / 8;                          // lanes per row
   constexpr int kRowsPass = kKvqThreads / kLanes;        // rows per pass of the CTA
-  constexpr int NR = TT / kRowsPass;                     // rows per lane: 4 or 2, or 1
+  constexpr int NR = TT / kRowsPass;                     // rows per lane: 4, 2 or 1
+  static_assert(2 * NR <= 8 && kLanes >= 8, "a lane for each row's parameters");
   constexpr int kPieces = TT / Y.ut;                     // V pieces per channel in a tile
   constexpr int kWords = Y.unit / 4;                     // words per V piece
   __shared__ __align__(16) uint32_t s_v[TT * kVStride<D> / 4];
@@ -183,44 +274,52 @@ __global__ void __launch_bounds__(kKvqThreads) kvq_store_kernel(const KvqParams 
         uint8_t* pg = p.pages + ((size_t)phys * p.Hkv + h) * Y.page_bytes;
         const int row0 = tid / kLanes, c8 = tid % kLanes;
         const int t0 = max(first - base, 0), t1 = min(end - base, TT);   // tokens of the tile written
-        float xk[NR][8], xv[NR][8];
+        Raw8<T> xk[NR], xv[NR];
 #pragma unroll
         for (int k = 0; k < NR; ++k) {
           const int t = row0 + k * kRowsPass;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) xk[k][i] = xv[k][i] = 0.f;
+          xk[k].zero();
+          xv[k].zero();
           if (t >= t0 && t < t1) {
             const size_t at = PACK ? (((size_t)src * p.Hkv + h) * P + in_page + t) * D + c8 * 8
                                    : (((size_t)b * p.n + (base + t - first)) * p.Hkv + h) * D + c8 * 8;
-            load8<T>(static_cast<const T*>(p.k_src) + at, xk[k]);
-            load8<T>(static_cast<const T*>(p.v_src) + at, xv[k]);
+            xk[k].load(static_cast<const T*>(p.k_src) + at);
+            xv[k].load(static_cast<const T*>(p.v_src) + at);
           }
         }
-        uint32_t code[NR][2], param[NR];
-        quantise_rows<D, BITS, NR>(xk, code, param);
+        // ranges of the 2 NR rows; then lane i of each row group works out the
+        // parameters of its i-th row, so that they cost one row's instructions
+        float mn = 0.f, mx = 0.f;
 #pragma unroll
-        for (int k = 0; k < NR; ++k) {
-          const int t = row0 + k * kRowsPass;
-          if (t < t0 || t >= t1) continue;
-          if (BITS == 4) {
-            // bytes (n0 n1 n2 n3) -> nibbles: (b | b >> 4) of each half-word
-            const uint32_t lo = code[k][0] | (code[k][0] >> 4), hi = code[k][1] | (code[k][1] >> 4);
-            *reinterpret_cast<uint32_t*>(pg + ((c8 >> 2) * P + in_page + t) * 16 + (c8 & 3) * 4) =
-                __byte_perm(lo, hi, 0x6420);
-          } else {
-            *reinterpret_cast<uint2*>(pg + ((c8 >> 1) * P + in_page + t) * 16 + (c8 & 1) * 8) =
-                make_uint2(code[k][0], code[k][1]);
+        for (int k = 0; k < 2 * NR; ++k) {
+          float a, e;
+          row_range<kLanes>(k < NR ? xk[k] : xv[k - NR], &a, &e);
+          if ((c8 & 7) == k) {
+            mn = a;
+            mx = e;
           }
-          if (c8 == 0) *reinterpret_cast<uint32_t*>(pg + Y.off_kp + (in_page + t) * 4) = param[k];
         }
-        quantise_rows<D, BITS, NR>(xv, code, param);
+        const KvqRow row = kvq_row<BITS>(mn, mx);
+        const int group = (tid & 31) & ~(kLanes - 1);
 #pragma unroll
-        for (int k = 0; k < NR; ++k) {
-          const int t = row0 + k * kRowsPass;
-          s_v[(t * kVStride<D>) / 4 + c8 * 2] = code[k][0];
-          s_v[(t * kVStride<D>) / 4 + c8 * 2 + 1] = code[k][1];
-          if (c8 == 0 && t >= t0 && t < t1)
-            *reinterpret_cast<uint32_t*>(pg + Y.off_vp + (in_page + t) * 4) = param[k];
+        for (int k = 0; k < 2 * NR; ++k) {
+          const int t = row0 + (k % NR) * kRowsPass;
+          const bool live = t >= t0 && t < t1;
+          const float z = __shfl_sync(0xffffffffu, row.z, group + k), s = __shfl_sync(0xffffffffu, row.s, group + k);
+          const float inv = __shfl_sync(0xffffffffu, row.inv, group + k);
+          uint32_t code[2], packed = 0u;
+          quantise8<T, BITS>(k < NR ? xk[k] : xv[k - NR], z, s, inv, code, &packed);
+          if (live && c8 == 0)
+            *reinterpret_cast<uint32_t*>(pg + (k < NR ? Y.off_kp : Y.off_vp) + (in_page + t) * 4) = pack_bf16x2(s, z);
+          if (k >= NR) {
+            s_v[(t * kVStride<D>) / 4 + c8 * 2] = code[0];
+            s_v[(t * kVStride<D>) / 4 + c8 * 2 + 1] = code[1];
+          } else if (live) {
+            if (BITS == 4)
+              *reinterpret_cast<uint32_t*>(pg + ((c8 >> 2) * P + in_page + t) * 16 + (c8 & 3) * 4) = packed;
+            else
+              *reinterpret_cast<uint2*>(pg + ((c8 >> 1) * P + in_page + t) * 16 + (c8 & 1) * 8) = make_uint2(code[0], code[1]);
+          }
         }
         __syncthreads();
         // four channels x eight tokens per step: lanes take 8 channel groups x 4 token groups

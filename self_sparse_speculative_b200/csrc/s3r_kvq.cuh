@@ -51,8 +51,8 @@ __host__ __device__ constexpr KvqLayout kvq_layout(int D, int P, int bits) {
 }
 
 struct KvqRow {
-  float z, s, inv;   // parameters (bf16 values) and 1 / s
-  bool flat;         // every n is 0
+  float z, s;   // parameters (bf16 values)
+  float inv;    // 1 / s; 0: every n is 0
 };
 
 // min and max that keep a NaN.
@@ -75,9 +75,8 @@ template <int BITS>
 __device__ __forceinline__ KvqRow kvq_row(float mn, float mx) {
   constexpr int kTop = (1 << BITS) - 1;
   KvqRow r;
-  r.flat = true;
   r.s = 1.f;
-  r.inv = 1.f;
+  r.inv = 0.f;
   if (!(mn > -INFINITY && mx < INFINITY)) {            // NaN or infinity in the row
     r.z = __int_as_float(0x7fc00000);
     return r;
@@ -89,24 +88,16 @@ __device__ __forceinline__ KvqRow kvq_row(float mn, float mx) {
   if (!(range < INFINITY) || (low > 0x7ff8u && low < 0x8008u)) q = (float)(((double)mx - (double)r.z) / kTop);
   const float s = __bfloat162float(__float2bfloat16_rn(q));
   if (s < kKvqTiny) return r;
-  r.flat = false;
   r.s = s;
   r.inv = __frcp_rn(s);
   return r;
 }
 
-// n of x. The float32 product is within 255 * 2^-22 of the quotient; nearer
-// than 2^-12 to a rounding border, or where x - z overflows, the float64
-// quotient decides.
+// n of x, from float64: (x - z) / s rounded to the nearest, ties to even.
 template <int BITS>
-__device__ __forceinline__ uint32_t kvq_number(float x, const KvqRow& r) {
+__device__ __forceinline__ uint32_t kvq_number_exact(float x, float z, float s) {
   constexpr int kTop = (1 << BITS) - 1;
-  if (r.flat) return 0u;
-  const float t = (x - r.z) * r.inv;
-  const float f = t + 12582912.f;                        // 1.5 * 2^23: rounds to the nearest whole, ties to even
-  int n = (int)(__float_as_uint(f) & 0x3fffffu);
-  const float d = t - (f - 12582912.f);
-  if (!(fabsf(d) <= 0.5f - 0.000244140625f)) n = __double2int_rn(((double)x - (double)r.z) / (double)r.s);
+  const int n = __double2int_rn(((double)x - (double)z) / (double)s);
   return (uint32_t)(n < kTop ? n : kTop);
 }
 
