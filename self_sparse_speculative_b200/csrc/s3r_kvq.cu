@@ -148,8 +148,9 @@ __device__ __noinline__ uint2 quantise8_exact(const Raw8<T> x, float z, float s)
 // The numbers of this lane's 8 channels, byte i of code = channel i; at 4 bits
 // also as 4 bytes of two. They are those of the exact quotient, ties to even:
 // - bf16: exact ties are common (8-bit values and steps). x - z is exact in
-//   float32 unless the two are more than 2^16 apart (tested: both ways back
-//   must be exact), and the quotient corrected by its remainder is the exact one
+//   float32 unless the two are more than 2^16 apart: (x - z) + z tells where x
+//   is the small one (that sum is exact then), `wide` where z is (a row at a
+//   time; it reaches the lanes as the sign of s). The quotient corrected by its remainder is the exact one
 //   rounded: it equals a border m + 1/2 only if the quotient does (it is off a
 //   border by at least 2^-17 of itself otherwise).
 // - float32: t = (x - z) (1 / s) is within 3 u t (u = 2^-24, t at most 2^BITS)
@@ -161,7 +162,8 @@ template <typename T, int BITS>
 __device__ __forceinline__ void quantise8(const Raw8<T>& x, float z, float s, float inv, uint32_t* code, uint32_t* packed) {
   constexpr float kMagic = 12582912.f;                   // 1.5 * 2^23: rounds to the nearest whole, ties to even
   constexpr bool kBf16 = sizeof(T) == 2;
-  uint32_t b[8], off = 0u;
+  uint32_t b[8], off = __float_as_uint(s) >> 31;         // (a wide row)
+  s = fabsf(s);
   float far = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -171,9 +173,7 @@ __device__ __forceinline__ void quantise8(const Raw8<T>& x, float z, float s, fl
     if (kBf16) {
       t = fma_pair(fma_pair(t, both(-s), d), both(inv), t);
       const float2 e = fma_pair(fma_pair(d, both(1.f), both(z)), both(-1.f), v);          // x - (d + z)
-      const float2 g = fma_pair(fma_pair(d, both(-1.f), v), both(1.f), both(-z));         // (x - d) - z
-      off |= __float_as_uint(e.x) | __float_as_uint(g.x);
-      off |= __float_as_uint(e.y) | __float_as_uint(g.y);
+      off |= __float_as_uint(e.x) | __float_as_uint(e.y);
     }
     float2 f = fma_pair(t, both(1.f), both(kMagic));
     if (!kBf16) {
@@ -229,7 +229,7 @@ __device__ __forceinline__ uint32_t token_mask(int w, int t0, int t1) {
 }
 
 template <typename T, int D, int P, int BITS, bool PACK>
-__global__ void __launch_bounds__(kKvqThreads) kvq_store_kernel(const KvqParams p) {
+__global__ void __launch_bounds__(kKvqThreads, sizeof(T) == 2 ? 8 : 4) kvq_store_kernel(const KvqParams p) {
   constexpr KvqLayout Y = kvq_layout(D, P, BITS);
   constexpr int TT = P == 64 ? 32 : 16;                  // tokens per tile
   constexpr int kLanes = D / 8;                          // lanes per row
@@ -305,12 +305,12 @@ __global__ void __launch_bounds__(kKvqThreads) kvq_store_kernel(const KvqParams 
         for (int k = 0; k < 2 * NR; ++k) {
           const int t = row0 + (k % NR) * kRowsPass;
           const bool live = t >= t0 && t < t1;
-          const float z = __shfl_sync(0xffffffffu, row.z, group + k), s = __shfl_sync(0xffffffffu, row.s, group + k);
+          const float z = __shfl_sync(0xffffffffu, row.z, group + k), s = __shfl_sync(0xffffffffu, row.wide ? -row.s : row.s, group + k);
           const float inv = __shfl_sync(0xffffffffu, row.inv, group + k);
           uint32_t code[2], packed = 0u;
           quantise8<T, BITS>(k < NR ? xk[k] : xv[k - NR], z, s, inv, code, &packed);
           if (live && c8 == 0)
-            *reinterpret_cast<uint32_t*>(pg + (k < NR ? Y.off_kp : Y.off_vp) + (in_page + t) * 4) = pack_bf16x2(s, z);
+            *reinterpret_cast<uint32_t*>(pg + (k < NR ? Y.off_kp : Y.off_vp) + (in_page + t) * 4) = pack_bf16x2(fabsf(s), z);
           if (k >= NR) {
             s_v[(t * kVStride<D>) / 4 + c8 * 2] = code[0];
             s_v[(t * kVStride<D>) / 4 + c8 * 2 + 1] = code[1];

@@ -53,6 +53,7 @@ __host__ __device__ constexpr KvqLayout kvq_layout(int D, int P, int bits) {
 struct KvqRow {
   float z, s;   // parameters (bf16 values)
   float inv;    // 1 / s; 0: every n is 0
+  bool wide;    // z is so much smaller than the largest value that x - z may lose its low bits in float32
 };
 
 // min and max that keep a NaN.
@@ -77,6 +78,7 @@ __device__ __forceinline__ KvqRow kvq_row(float mn, float mx) {
   KvqRow r;
   r.s = 1.f;
   r.inv = 0.f;
+  r.wide = false;
   if (!(mn > -INFINITY && mx < INFINITY)) {            // NaN or infinity in the row
     r.z = __int_as_float(0x7fc00000);
     return r;
@@ -90,6 +92,7 @@ __device__ __forceinline__ KvqRow kvq_row(float mn, float mx) {
   if (s < kKvqTiny) return r;
   r.s = s;
   r.inv = __frcp_rn(s);
+  r.wide = fabsf(r.z) < 0x1p-15f * mx && r.z != 0.f;
   return r;
 }
 

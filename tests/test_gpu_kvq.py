@@ -221,3 +221,33 @@ def test_bad_lengths_and_pages_are_flagged_and_nothing_else_is_touched():
                 Q.write_row(before[table[b, p], h], D, P, bits, t, kh[i, h, t], kh[i, h, t])
     assert np.array_equal(dev["pages"].cpu().numpy(), before)
     assert s3r.s3r_device_status(dev["ws"])[1] == s3r.S3R_DEV_BAD_CONTEXT_LEN | s3r.S3R_DEV_BAD_PAGE_ID
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_bf16_values_far_apart_in_size(bits):
+    # bf16 rows whose differences x - z are not exact in float32 (tiny x beside a large minimum, a tiny minimum
+    # beside large x), next to and on rounding borders of the large part
+    D, P, H = 64, 64, 1
+    rng = np.random.default_rng(3)
+    xs = []
+    for i in range(256):
+        top = 2 ** bits - 1
+        s = Q.bf16_value(Q.bf16_nearest(np.float32(np.exp(rng.uniform(-3, 3)))))
+        x = (s * rng.integers(0, 2 * top + 1, D) / 2).astype(np.float32)       # halves of steps: ties
+        x[0], x[1] = 0, s * top
+        tiny = (rng.choice([-1, 1], D) * np.exp(rng.uniform(-30, -8, D))).astype(np.float32)
+        if i % 3 == 0:
+            x = x - np.float32(s * (rng.integers(0, top) + 0.5))               # a border at zero: tiny values beside it
+            x[2:12] = tiny[2:12]
+        elif i % 3 == 1:
+            x[0] = abs(tiny[0]) if i % 2 else -abs(tiny[0])                    # a tiny minimum
+        xs.append(x)
+    x = Q.bf16_value(Q.bf16_nearest(np.stack(xs))).astype(np.float32)
+    n = len(x)
+    width = n // P
+    pages, table, dev = cache(1, H, D, P, bits, [0], width, seed=2)
+    k = torch.from_numpy(x.reshape(1, n, H, D)).to(torch.bfloat16).cuda()
+    s3r.s3r_kvq_append(dev["kvq"], dev["lens"], k, k, "bf16", n, 0, dev["ws"])
+    Q.append(pages, table, [0], x.reshape(1, n, H, D), x.reshape(1, n, H, D), bits, P, 0)
+    assert np.array_equal(dev["pages"].cpu().numpy(), pages)
+    ok(dev)
