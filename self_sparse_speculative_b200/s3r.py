@@ -314,36 +314,45 @@ def s3r_kvq_page_bytes(head_dim: int, page_size: int, bits: int) -> int:
     return int(_lib.s3r_kvq_page_bytes(int(head_dim), int(page_size), int(bits)))
 
 
-def _expect(name, x, dtype, shape):
-    """A tensor argument the library would read or write past if its type, shape or layout were another."""
-    if x is None or isinstance(x, int):
-        return
-    if tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {x.dtype} {tuple(x.shape)}")
-    if x.is_cuda:
+_torch = None
+
+
+def _expect(device, *args):
+    """Checks (name, tensor, dtype, shape) arguments: the library would read or write past a tensor of another type,
+    shape or layout. device: index of the current device. None and raw addresses pass."""
+    for name, x, dtype, shape in args:
+        if x is None or isinstance(x, int):
+            continue
+        if x.shape != shape or x.dtype != dtype or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                             f"got {x.dtype} {tuple(x.shape)}")
+        if not x.is_cuda:
+            raise ValueError(f"{name} must live on the GPU")
+        if x.get_device() != device:
+            raise ValueError(f"{name} lives on {x.device}, the current device is cuda:{device}")
+
+
+def _kvq_env(dtype):
+    """(current device index, torch dtype, its code); -1 without a GPU."""
+    global _torch
+    if _torch is None:
         import torch
-        if x.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} lives on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
-    else:
-        raise ValueError(f"{name} must live on the GPU")
-
-
-def _torch_dtype(dtype):
-    import torch
-    return torch.bfloat16 if dtype_code(dtype) == S3R_BF16 else torch.float32
+        _torch = torch
+    code = dtype_code(dtype) if dtype is not None else S3R_BF16
+    device = _torch.cuda.current_device() if _torch.cuda.is_available() else -1
+    return device, _torch.bfloat16 if code == S3R_BF16 else _torch.float32, code
 
 
 def paged_kvq(pages, block_table, context_lens, num_q_heads: int, head_dim: int, page_size: int, bits: int) -> PagedKVQ:
     """Describe a quantised cache: pages uint8 [num_pages_total, Hkv, s3r_kvq_page_bytes(D, P, bits)]."""
-    import torch
+    device, _, _ = _kvq_env(None)
     n, h, nb = pages.shape
     if nb != s3r_kvq_page_bytes(head_dim, page_size, bits):
         raise ValueError(f"pages have {nb} bytes per head, head_dim {head_dim}, page_size {page_size} and {bits} bits "
                          f"need {s3r_kvq_page_bytes(head_dim, page_size, bits)}")
-    _expect("pages", pages, torch.uint8, (n, h, nb))
-    _expect("block_table", block_table, torch.int32, block_table.shape)
-    _expect("context_lens", context_lens, torch.int32, (block_table.shape[0],))
+    _expect(device, ("pages", pages, _torch.uint8, (n, h, nb)),
+            ("block_table", block_table, _torch.int32, block_table.shape),
+            ("context_lens", context_lens, _torch.int32, (block_table.shape[0],)))
     kvq = PagedKVQ(int(block_table.shape[0]), int(num_q_heads), int(h), int(head_dim), int(page_size),
                    int(block_table.shape[1]), int(n), int(bits), _ptr(pages), _ptr(block_table), _ptr(context_lens))
     kvq.tensors = (pages, block_table, context_lens)     # alive as long as the description
@@ -354,10 +363,10 @@ def s3r_kvq_append(kvq: PagedKVQ, context_lens, k_new, v_new, dtype, n: int, ove
                    workspace_bytes=None, stream=None):
     """Quantise n rows per sequence into positions L - overwrite.. (updating L; context_lens None: L stays)."""
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    device, dt, code = _kvq_env(dtype)
     shape = (kvq.num_seqs, n, kvq.num_kv_heads, kvq.head_dim)
-    _expect("k_new", k_new, _torch_dtype(dtype), shape)
-    _expect("v_new", v_new, _torch_dtype(dtype), shape)
-    st = _lib.s3r_kvq_append(ctypes.byref(kvq), _ptr(context_lens), _ptr(k_new), _ptr(v_new), dtype_code(dtype), int(n),
+    _expect(device, ("k_new", k_new, dt, shape), ("v_new", v_new, dt, shape))
+    st = _lib.s3r_kvq_append(ctypes.byref(kvq), _ptr(context_lens), _ptr(k_new), _ptr(v_new), code, int(n),
                              int(overwrite), _ptr(workspace), wb, _stream(stream))
     _check("s3r_kvq_append", st)
 
@@ -371,22 +380,20 @@ def s3r_kvq_pack(kv: PagedKV, kvq: PagedKVQ, last_n: int, workspace, workspace_b
 
 def s3r_kvq_read(kvq: PagedKVQ, start, n: int, dtype, k_out, v_out, workspace, workspace_bytes=None, stream=None):
     """Positions start[b] + t (start None: 0) of each sequence to rows k_out[b, t], v_out[b, t]."""
-    import torch
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    device, dt, code = _kvq_env(dtype)
     shape = (kvq.num_seqs, n, kvq.num_kv_heads, kvq.head_dim)
-    _expect("start", start, torch.int32, (kvq.num_seqs,))
-    _expect("k_out", k_out, _torch_dtype(dtype), shape)
-    _expect("v_out", v_out, _torch_dtype(dtype), shape)
-    st = _lib.s3r_kvq_read(ctypes.byref(kvq), _ptr(start), int(n), dtype_code(dtype), _ptr(k_out), _ptr(v_out),
+    _expect(device, ("start", start, _torch.int32, (kvq.num_seqs,)), ("k_out", k_out, dt, shape), ("v_out", v_out, dt, shape))
+    st = _lib.s3r_kvq_read(ctypes.byref(kvq), _ptr(start), int(n), code, _ptr(k_out), _ptr(v_out),
                            _ptr(workspace), wb, _stream(stream))
     _check("s3r_kvq_read", st)
 
 
 def s3r_kvq_rollback(kvq: PagedKVQ, context_lens, num_accepted, rows: int, workspace, workspace_bytes=None, stream=None):
     """L <- L - rows + n_acc + 1."""
-    import torch
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
-    _expect("num_accepted", num_accepted, torch.int32, (kvq.num_seqs,))
+    device, _, _ = _kvq_env(None)
+    _expect(device, ("num_accepted", num_accepted, _torch.int32, (kvq.num_seqs,)))
     st = _lib.s3r_kvq_rollback(ctypes.byref(kvq), _ptr(context_lens), _ptr(num_accepted), int(rows), _ptr(workspace), wb,
                                _stream(stream))
     _check("s3r_kvq_rollback", st)
@@ -399,14 +406,12 @@ def s3r_kvq_attn_workspace_bytes(kvq: PagedKVQ, dtype, rows: int, budget_pages: 
 def s3r_kvq_attn(kvq: PagedKVQ, q, dtype, rows: int, scale: float, out, lse, workspace, pages=None, budget_pages: int = 0,
                  workspace_bytes=None, stream=None):
     """Causal attention of `rows` rows per sequence over the quantised cache (pages: the list of kept pages, or all)."""
-    import torch
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    device, dt, code = _kvq_env(dtype)
     shape = (kvq.num_seqs, rows, kvq.num_q_heads, kvq.head_dim)
-    _expect("q", q, _torch_dtype(dtype), shape)
-    _expect("out", out, _torch_dtype(dtype), shape)
-    _expect("lse", lse, torch.float32, shape[:3])
-    _expect("pages", pages, torch.int32, (kvq.num_seqs, kvq.num_kv_heads, budget_pages))
-    st = _lib.s3r_kvq_attn(ctypes.byref(kvq), _ptr(q), dtype_code(dtype), int(rows), _ptr(pages), int(budget_pages),
+    _expect(device, ("q", q, dt, shape), ("out", out, dt, shape), ("lse", lse, _torch.float32, shape[:3]),
+            ("pages", pages, _torch.int32, (kvq.num_seqs, kvq.num_kv_heads, budget_pages)))
+    st = _lib.s3r_kvq_attn(ctypes.byref(kvq), _ptr(q), code, int(rows), _ptr(pages), int(budget_pages),
                            float(scale), _ptr(out), _ptr(lse), _ptr(workspace), wb, _stream(stream))
     _check("s3r_kvq_attn", st)
 
