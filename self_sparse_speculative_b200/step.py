@@ -42,7 +42,8 @@ def torch_dtype(dtype: str):
 class DecodeStep:
     """Device-resident inputs, outputs and workspaces of one round."""
 
-    def __init__(self, wl: Workload, device="cuda", upload_chunk_pages: int = 2048):
+    def __init__(self, wl: Workload, device="cuda", upload_chunk_pages: int = 2048, draft_bits: int | None = None):
+        """draft_bits (4 or 8): also keep the cache in that many bits, for round_quantised()'s drafts."""
         self.wl = wl
         ws = wl.spec
         self.device = torch.device(device)
@@ -102,6 +103,13 @@ class DecodeStep:
         self.ws_tokens = self._ws(s3r.s3r_sample_workspace_bytes(S * g, 0, V))
         self.ws_sample = self._ws(s3r.s3r_sample_workspace_bytes(S, g, V))
         self.scale = wl.scale
+        self.kvq = None
+        if draft_bits is not None:
+            # the copy shares the block table and the lengths
+            self.pages_q = torch.zeros((n, Hkv, s3r.s3r_kvq_page_bytes(D, P, draft_bits)), dtype=torch.uint8, device=dev)
+            self.kvq = s3r.paged_kvq(self.pages_q, self.block_table, self.context_lens, Hq, D, P, draft_bits)
+            self.ws_kvq = self._ws(s3r.s3r_kv_workspace_bytes(S))
+            self.ws_draft_q = self._ws(s3r.s3r_kvq_attn_workspace_bytes(self.kvq, ws.kv_dtype, 1))
 
     def _ws(self, nbytes: int) -> torch.Tensor:
         assert nbytes > 0, "workspace query rejected the shapes"
@@ -171,6 +179,42 @@ class DecodeStep:
         s3r.s3r_kv_rollback(self.kv, self.context_lens, self.num_accepted, R, self.kmin, self.kmax, self.ws_kv,
                             stream=stream)
 
+    def quantise(self, last_n: int = 0, stream=None):
+        """The cache's last last_n positions (0: all) into its quantised copy."""
+        s3r.s3r_kvq_pack(self.kv, self.kvq, last_n, self.ws_kvq, stream=stream)
+
+    def draft_quantised(self, i: int, stream=None):
+        """Draft step i over every page of the quantised copy."""
+        ws = self.wl.spec
+        s3r.s3r_kvq_attn(self.kvq, self.q_draft[i].unsqueeze(1), ws.kv_dtype, 1, self.scale, self.draft_out[i].unsqueeze(1),
+                         self.draft_lse[i].unsqueeze(1), self.ws_draft_q, stream=stream)
+
+    def round_quantised(self, stream=None):
+        """round_with_kv() with the drafts attending over the quantised copy instead of selected pages: each step's
+        rows go to the copy and to the cache (the copy first: it takes the positions from the shared lengths),
+        verification and sampling are those of every round, and the verifier's rows replace the drafter's in both.
+        The copy holds the committed positions beforehand (quantise())."""
+        ws = self.wl.spec
+        g, R = ws.gamma, ws.rows
+        st = torch.cuda.current_stream(self.device) if stream is None else stream
+        with torch.cuda.stream(st):
+            self.context_lens.copy_(self.lens_committed)
+        self.draw_draft_tokens(stream)
+
+        def store(k, v, n, overwrite):
+            s3r.s3r_kvq_append(self.kvq, None, k, v, ws.kv_dtype, n, overwrite, self.ws_kvq, stream=stream)
+            s3r.s3r_kv_append(self.kv, self.context_lens, k, v, n, overwrite, self.kmin, self.kmax, self.ws_kv,
+                              stream=stream)
+
+        for i in range(g):
+            store(self.k_round_draft[i], self.v_round_draft[i], 1, 0)
+            self.draft_quantised(i, stream)
+        store(self.k_round_verify, self.v_round_verify, R, g)
+        self.verify(stream)
+        self.sample(stream)
+        s3r.s3r_kv_rollback(self.kv, self.context_lens, self.num_accepted, R, self.kmin, self.kmax, self.ws_kv,
+                            stream=stream)
+
     def capture_round(self):
         """One whole round captured into a CUDA graph. The library's kernels
         chain by programmatic dependent launch, which the capture keeps as
@@ -188,7 +232,8 @@ class DecodeStep:
     def device_checks(self):
         """Status words of every workspace (synchronises)."""
         return {name: s3r.s3r_device_status(getattr(self, name))
-                for name in ("ws_draft", "ws_verify", "ws_tokens", "ws_sample", "ws_kv")}
+                for name in ("ws_draft", "ws_verify", "ws_tokens", "ws_sample", "ws_kv")
+                + (("ws_kvq", "ws_draft_q") if self.kvq is not None else ())}
 
     # ---------------------------------------------------------------- bytes
     def algorithmic_bytes(self):
