@@ -46,6 +46,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "s3r_attn_common.cuh"
 #include "s3r_attn_sched.cuh"
@@ -70,7 +71,7 @@ constexpr int kProducer = 16, kMmaQk = 17, kMmaPv = 18;
 // two terms of a row in columns NRT apart.
 template <int NR, bool ALT, int D, int BITS>
 struct Lay {
-  static constexpr bool E4 = BITS == 4 && ALT;
+  static constexpr bool E4 = BITS == 4 && ALT && NR <= 16;
   static constexpr int NRT = ALT ? NR : 2 * NR;
   static constexpr int N = ((E4 ? 2 * NRT : NRT) + 15) / 16 * 16;
   static constexpr int kTile = E4 ? 32 : 64;               // TMEM columns of 128 numbers a lane
@@ -87,7 +88,7 @@ struct Lay {
   static constexpr int NSB = 4 * kTile + (4 + kO) * N <= 512 ? 4 : 2;
   static constexpr int kFit = (512 - (NSB + kO) * N) / (2 * kTile);
   static constexpr int NB = kFit >= 4 ? 4 : 2;
-  static constexpr int kNT = E4 ? NB : NB + NSB <= 4 ? 4 : 8;   // stages of tokens' parameters
+  static constexpr int kNT = E4 ? NB : 4;                  // stages of tokens' parameters
   static constexpr int NKE = NB > NSB ? NB : NSB;          // products of keys whose completion may still be waited for
   static constexpr uint32_t kColK = 0, kColV = kTile * NB, kColS = 2 * kTile * NB, kColO = kColS + NSB * N;
   static constexpr uint32_t kOffT = kOffX + kXBytes;       // tokens' parameters: float4 [128], float2 [128] a stage
@@ -100,7 +101,7 @@ struct Lay {
   static constexpr float kTop = E4 ? 6.f : 8.f, kTau = E4 ? 2.f : 7.f;
   static_assert(kNSraw >= 2, "the ring needs two stages");
   static_assert(NB >= 2 && 2 * kTile * NB + (NSB + kO) * N <= 512, "TMEM columns");
-  static_assert(E4 || kNT >= NB + NSB, "a token's parameters outlive the stages in flight");
+  static_assert(E4 || kNT >= NB + 2, "parameters are written at most NB + 1 stages after the last product that used their place");
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, f32 accumulate: 32 of k of e4m3 or 16 of f16.
@@ -142,16 +143,7 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
 }
-// 16 registers to this warp's TMEM lanes, 16 consecutive columns.
-__device__ __forceinline__ void tmem_st16_raw(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// 32 registers to this warp's TMEM lanes, 32 consecutive columns.
+// 32 (16) registers to this warp's TMEM lanes, as many consecutive columns.
 __device__ __forceinline__ void tmem_st32_raw(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -161,6 +153,14 @@ __device__ __forceinline__ void tmem_st32_raw(uint32_t taddr, const uint32_t* r)
          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16_raw(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 // 1-D bulk copy global -> this CTA's shared memory with an L2 policy.
@@ -605,16 +605,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     // E4: the warpgroups take alternate stages, keys and values, so that a
     // warpgroup's chain of waits, loads and stores spans two stages; the tiles
     // and parameters of stage g - NB are free once its product of values is
-    // done. Else (two or three tiles in TMEM): one takes the keys and
-    // parameters, one the values, so that keys run ahead of the softmax (5 rows
-    // of 16 x 16384 tokens in 8 bits: 146 us, alternating 160).
+    // done. Else (two tiles in TMEM): one takes the keys, one the values and
+    // parameters, so that keys run ahead of the softmax (5 rows of 16 x 16384
+    // tokens in 8 bits: 146 us, alternating 160).
     split_registers<false>();
     const int uwg = (warp - 8) >> 2;
     const int t = tid & 127;                             // TMEM lane: token of S^T, channel of O^T
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
     constexpr int kWordsPage = P * BITS / 32;            // words of a channel in one page: 2, 4, 8 or 16
-    constexpr int kHalfWords = 64 * BITS / 32;           // f16: words of 32 columns' numbers, 8 or 16
-    int Lb = -1, of = -1;                                // length of sequence `of`
+      int Lb = -1, of = -1;                                // length of sequence `of`
+    // Words of a row (16-byte reads) to columns of this lane, 16 columns (8 bits:
+    // 32) a turn of a rolled loop: five roles run on every SM quadrant at once and
+    // instruction fetch, not arithmetic, bounds them (unrolled, 48 rows of 4-bit
+    // tokens took 1800 ns a stage instead of 1590).
+    auto unpack_columns = [&](auto values, auto cols, auto words, uint32_t dst) {
+      constexpr int kCols = decltype(cols)::value, kTurn = BITS == 8 && kCols >= 32 ? 32 : 16;
+      constexpr int kWords = (E4 ? 8 : BITS) * kTurn / 16;   // words of a turn
+#pragma unroll 1
+      for (int c = 0; c < kCols / kTurn; ++c) {
+        uint32_t r[kTurn];
+#pragma unroll
+        for (int k = 0; k < kWords; k += 4) {
+          const uint4 w = words(c * kWords + k);
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (E4) unpack_e4<decltype(values)::value>(v[i], r + 2 * (k + i));
+            else unpack<BITS>(v[i], r + (k + i) * (16 / BITS));
+          }
+        }
+        if constexpr (kTurn == 32) tmem_st32_raw(dst + c * 32, r);
+        else tmem_st16_raw(dst + c * 16, r);
+      }
+    };
     for (Walk c = walk_begin(p, s_prefix, lo, hi, W, ppt); c.valid; walk_next(p, s_prefix, hi, W, ppt, c)) {
       const uint32_t g = c.g, st = g % NS, buf = g % NB;
       if (E4 && (g & 1u) != (uint32_t)uwg) continue;
@@ -623,83 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         Lb = p.context_lens[of];
       }
       bool ok = mbar_wait(BAR(B_FULL + st), (g / NS) & 1, &s_abort, p.status);
-      if (g >= NB) {
-        const uint32_t x = g - NB;
-        ok = ok && (E4 || uwg == 1 ? mbar_wait(BAR(B_VE + buf), (x / NB) & 1, &s_abort, p.status)
-                                   : mbar_wait(BAR(B_KE + x % NKE), (x / NKE) & 1, &s_abort, p.status));
-      }
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
       const uint8_t* const stage = sKV + st * L::kStage;
-      if (E4 || uwg == 0) {
-        const uint32_t dst = tmem + lane_base + L::kColK + buf * L::kTile;
-        const uint8_t* const row = stage + (t / P) * Y.page_bytes + (t % P) * 16;
-        auto words = [&](int k) { return *reinterpret_cast<const uint4*>(row + (k / 4) * (P * 16)); };
-#pragma unroll
-        for (int half = 0; half < L::kKCols / 32 || half < 1; ++half) {
-          uint32_t r[32];
-          if constexpr (E4) {
-#pragma unroll
-            for (int k = 0; k < L::kKCols / 2; k += 4) {
-              const uint4 w = words(k);
-              unpack_e4<false>(w.x, r + 2 * k);
-              unpack_e4<false>(w.y, r + 2 * k + 2);
-              unpack_e4<false>(w.z, r + 2 * k + 4);
-              unpack_e4<false>(w.w, r + 2 * k + 6);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < kHalfWords; k += 4) {
-              const uint4 w = words(half * kHalfWords + k);
-              unpack<BITS>(w.x, r + k * 16 / BITS);
-              unpack<BITS>(w.y, r + (k + 1) * 16 / BITS);
-              unpack<BITS>(w.z, r + (k + 2) * 16 / BITS);
-              unpack<BITS>(w.w, r + (k + 3) * 16 / BITS);
-            }
-          }
-          if constexpr (L::kKCols >= 32) tmem_st32_raw(dst + half * 32, r);
-          else tmem_st16_raw(dst, r);
-        }
-      }
-      if ((E4 || uwg == 1) && (D == 128 || t < D)) {     // whole warps; lanes past D hold anything and are never read
-        const uint32_t dst = tmem + lane_base + L::kColV + buf * L::kTile;
-        auto words = [&](int k) {
-          const int pg = k / kWordsPage;
-          if constexpr (kUnit == 16)
-            return *reinterpret_cast<const uint4*>(stage + pg * Y.page_bytes + Y.off_v + (k % kWordsPage / 4 * D + t) * 16);
-          const uint2 v0 = *reinterpret_cast<const uint2*>(stage + pg * Y.page_bytes + Y.off_v + t * 8);   // two pages of two words
-          const uint2 v1 = *reinterpret_cast<const uint2*>(stage + (pg + 1) * Y.page_bytes + Y.off_v + t * 8);
-          return make_uint4(v0.x, v0.y, v1.x, v1.y);
-        };
-#pragma unroll
-        for (int half = 0; half < L::kTile / 32; ++half) {
-          uint32_t r[32];
-          if constexpr (E4) {
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const uint4 w = words(k);
-              unpack_e4<true>(w.x, r + 2 * k);
-              unpack_e4<true>(w.y, r + 2 * k + 2);
-              unpack_e4<true>(w.z, r + 2 * k + 4);
-              unpack_e4<true>(w.w, r + 2 * k + 6);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < kHalfWords; k += 4) {
-              const uint4 w = words(half * kHalfWords + k);
-              unpack<BITS>(w.x, r + k * 16 / BITS);
-              unpack<BITS>(w.y, r + (k + 1) * 16 / BITS);
-              unpack<BITS>(w.z, r + (k + 2) * 16 / BITS);
-              unpack<BITS>(w.w, r + (k + 3) * 16 / BITS);
-            }
-          }
-          tmem_st32_raw(dst + half * 32, r);
-        }
-      }
       // the token's parameters for the softmax: y = ka S^T + kb sum q (scaled),
       // log2 s_v, 1 / s_v, the centre of its values over s_v, and its position
       // against the rows' (hidden from rows before `excess`; from all: kHidden)
-      if (E4 || uwg == 0) {
+      auto token_parameters = [&]() {
         const uint8_t* pg = stage + (t / P) * Y.page_bytes;
         const uint32_t kp = *reinterpret_cast<const uint32_t*>(pg + Y.off_kp + (t % P) * 4);
         const uint32_t vp = *reinterpret_cast<const uint32_t*>(pg + Y.off_vp + (t % P) * 4);
@@ -716,15 +667,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         reinterpret_cast<float4*>(at)[t] = make_float4(p.scale_log2 * sk, p.scale_log2 * fmaf(kMid, sk, zk), __log2f(sv), rsv);
         reinterpret_cast<float2*>(at + 128 * 16)[t] =
             make_float2(zc, __int_as_float(valid ? pos - (Lb - p.R) - p.r0 : kHidden));
+      };
+      if (!E4 && uwg == 1) {
+        // ahead of the values: the softmax needs them with S^T
+        token_parameters();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_TF + g % kNT));
       }
+      if (g >= NB) {
+        const uint32_t x = g - NB;
+        ok = ok && (E4 || uwg == 1 ? mbar_wait(BAR(B_VE + buf), (x / NB) & 1, &s_abort, p.status)
+                                   : mbar_wait(BAR(B_KE + x % NKE), (x / NKE) & 1, &s_abort, p.status));
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (E4 || uwg == 0) {
+        const uint32_t dst = tmem + lane_base + L::kColK + buf * L::kTile;
+        const uint8_t* const row = stage + (t / P) * Y.page_bytes + (t % P) * 16;
+        auto words = [&](int k) { return *reinterpret_cast<const uint4*>(row + (k / 4) * (P * 16)); };
+        unpack_columns(std::false_type{}, std::integral_constant<int, L::kKCols>{}, words, dst);
+      }
+      if ((E4 || uwg == 1) && (D == 128 || t < D)) {     // whole warps; lanes past D hold anything and are never read
+        const uint32_t dst = tmem + lane_base + L::kColV + buf * L::kTile;
+        auto words = [&](int k) {
+          const int pg = k / kWordsPage;
+          if constexpr (kUnit == 16)
+            return *reinterpret_cast<const uint4*>(stage + pg * Y.page_bytes + Y.off_v + (k % kWordsPage / 4 * D + t) * 16);
+          const uint2 v0 = *reinterpret_cast<const uint2*>(stage + pg * Y.page_bytes + Y.off_v + t * 8);   // two pages of two words
+          const uint2 v1 = *reinterpret_cast<const uint2*>(stage + (pg + 1) * Y.page_bytes + Y.off_v + t * 8);
+          return make_uint4(v0.x, v0.y, v1.x, v1.y);
+        };
+        unpack_columns(std::true_type{}, std::integral_constant<int, L::kTile>{}, words, dst);
+      }
+      if constexpr (E4) token_parameters();
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (E4 || uwg == 0) {
-          mbar_arrive(BAR(B_KF + buf));
-          mbar_arrive(BAR(B_TF + g % kNT));
-        }
+        if (E4 || uwg == 0) mbar_arrive(BAR(B_KF + buf));
+        if (E4) mbar_arrive(BAR(B_TF + g % kNT));
         if (E4 || uwg == 1) mbar_arrive(BAR(B_VF + buf));
         mbar_arrive(BAR(B_EMPTY + st));
       }
