@@ -333,14 +333,23 @@ def _expect(device, *args):
 
 
 def _kvq_env(dtype):
-    """(current device index, torch dtype, its code); -1 without a GPU."""
+    """(current device index, torch dtype, its code); -1 before CUDA is in use (there are no GPU tensors then)."""
     global _torch
     if _torch is None:
         import torch
         _torch = torch
     code = dtype_code(dtype) if dtype is not None else S3R_BF16
-    device = _torch.cuda.current_device() if _torch.cuda.is_available() else -1
+    device = _torch.cuda.current_device() if _torch.cuda.is_initialized() else -1
     return device, _torch.bfloat16 if code == S3R_BF16 else _torch.float32, code
+
+
+def _stream_on(stream, device):
+    """_stream(stream), without building a stream object for the current one (3 us of a small call)."""
+    if stream is None and device >= 0:
+        raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(device)
+    return _stream(stream)
 
 
 def paged_kvq(pages, block_table, context_lens, num_q_heads: int, head_dim: int, page_size: int, bits: int) -> PagedKVQ:
@@ -367,14 +376,15 @@ def s3r_kvq_append(kvq: PagedKVQ, context_lens, k_new, v_new, dtype, n: int, ove
     shape = (kvq.num_seqs, n, kvq.num_kv_heads, kvq.head_dim)
     _expect(device, ("k_new", k_new, dt, shape), ("v_new", v_new, dt, shape))
     st = _lib.s3r_kvq_append(ctypes.byref(kvq), _ptr(context_lens), _ptr(k_new), _ptr(v_new), code, int(n),
-                             int(overwrite), _ptr(workspace), wb, _stream(stream))
+                             int(overwrite), _ptr(workspace), wb, _stream_on(stream, device))
     _check("s3r_kvq_append", st)
 
 
 def s3r_kvq_pack(kv: PagedKV, kvq: PagedKVQ, last_n: int, workspace, workspace_bytes=None, stream=None):
     """Quantise the last last_n positions (0: all) of each sequence of kv into kvq."""
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
-    st = _lib.s3r_kvq_pack(ctypes.byref(kv), ctypes.byref(kvq), int(last_n), _ptr(workspace), wb, _stream(stream))
+    device, _, _ = _kvq_env(None)
+    st = _lib.s3r_kvq_pack(ctypes.byref(kv), ctypes.byref(kvq), int(last_n), _ptr(workspace), wb, _stream_on(stream, device))
     _check("s3r_kvq_pack", st)
 
 
@@ -385,7 +395,7 @@ def s3r_kvq_read(kvq: PagedKVQ, start, n: int, dtype, k_out, v_out, workspace, w
     shape = (kvq.num_seqs, n, kvq.num_kv_heads, kvq.head_dim)
     _expect(device, ("start", start, _torch.int32, (kvq.num_seqs,)), ("k_out", k_out, dt, shape), ("v_out", v_out, dt, shape))
     st = _lib.s3r_kvq_read(ctypes.byref(kvq), _ptr(start), int(n), code, _ptr(k_out), _ptr(v_out),
-                           _ptr(workspace), wb, _stream(stream))
+                           _ptr(workspace), wb, _stream_on(stream, device))
     _check("s3r_kvq_read", st)
 
 
@@ -395,7 +405,7 @@ def s3r_kvq_rollback(kvq: PagedKVQ, context_lens, num_accepted, rows: int, works
     device, _, _ = _kvq_env(None)
     _expect(device, ("num_accepted", num_accepted, _torch.int32, (kvq.num_seqs,)))
     st = _lib.s3r_kvq_rollback(ctypes.byref(kvq), _ptr(context_lens), _ptr(num_accepted), int(rows), _ptr(workspace), wb,
-                               _stream(stream))
+                               _stream_on(stream, device))
     _check("s3r_kvq_rollback", st)
 
 
@@ -412,7 +422,7 @@ def s3r_kvq_attn(kvq: PagedKVQ, q, dtype, rows: int, scale: float, out, lse, wor
     _expect(device, ("q", q, dt, shape), ("out", out, dt, shape), ("lse", lse, _torch.float32, shape[:3]),
             ("pages", pages, _torch.int32, (kvq.num_seqs, kvq.num_kv_heads, budget_pages)))
     st = _lib.s3r_kvq_attn(ctypes.byref(kvq), _ptr(q), code, int(rows), _ptr(pages), int(budget_pages),
-                           float(scale), _ptr(out), _ptr(lse), _ptr(workspace), wb, _stream(stream))
+                           float(scale), _ptr(out), _ptr(lse), _ptr(workspace), wb, _stream_on(stream, device))
     _check("s3r_kvq_attn", st)
 
 
