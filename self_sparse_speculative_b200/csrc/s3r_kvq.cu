@@ -16,7 +16,7 @@
 // and 16 for 16-token ones: a tile then holds whole V pieces, so the V bytes
 // of a tile belong to one CTA and no two CTAs of a call write the same byte.
 // A row is D/8 lanes of 8 channels (16-byte loads of bf16); minimum and maximum meet
-// by shuffles. K numbers go out as they are; V numbers turn channel-major
+// by shuffles; with small rows or pages a CTA takes two or four tiles. K numbers go out as they are; V numbers turn channel-major
 // through shared memory, four channels by eight tokens per thread with byte
 // permutes, and leave as 16-byte pieces. A V piece of which only some tokens
 // are written keeps the other tokens' bits.
@@ -228,18 +228,30 @@ __device__ __forceinline__ uint32_t token_mask(int w, int t0, int t1) {
   return below_b & ~below_a;
 }
 
+// How a CTA is cut: tiles of TT tokens, kT threads each, four rows a lane.
+template <int D, int P, int BITS>
+struct Cut {
+  static constexpr KvqLayout Y = kvq_layout(D, P, BITS);
+  static constexpr int TT = P == 64 ? 32 : 16;           // tokens per tile
+  static constexpr int kLanes = D / 8;                   // lanes per row
+  static constexpr int NR = 4;                           // rows per lane
+  static constexpr int kT = TT * kLanes / NR;            // threads per tile: 32, 64 or 128
+  static constexpr int kTiles = kKvqThreads / kT;        // tiles per CTA
+  static constexpr int kRowsPass = kT / kLanes;          // rows per pass of a tile's threads
+  static constexpr int kPieces = TT / Y.ut;              // V pieces per channel in a tile
+  static constexpr int kTg = TT / 8;                     // groups of eight tokens
+  static constexpr int kVWords = TT * kVStride<D> / 4;
+};
+
 template <typename T, int D, int P, int BITS, bool PACK>
 __global__ void __launch_bounds__(kKvqThreads, sizeof(T) == 2 ? 8 : 4) kvq_store_kernel(const KvqParams p) {
-  constexpr KvqLayout Y = kvq_layout(D, P, BITS);
-  constexpr int TT = P == 64 ? 32 : 16;                  // tokens per tile
-  constexpr int kLanes = D / 8;                          // lanes per row
-  constexpr int kRowsPass = kKvqThreads / kLanes;        // rows per pass of the CTA
-  constexpr int NR = TT / kRowsPass;                     // rows per lane: 4, 2 or 1
-  static_assert(2 * NR <= 8 && kLanes >= 8, "a lane for each row's parameters");
-  constexpr int kPieces = TT / Y.ut;                     // V pieces per channel in a tile
+  using G = Cut<D, P, BITS>;
+  constexpr KvqLayout Y = G::Y;
+  constexpr int TT = G::TT, kLanes = G::kLanes, NR = G::NR, kT = G::kT, kRowsPass = G::kRowsPass, kPieces = G::kPieces;
   constexpr int kWords = Y.unit / 4;                     // words per V piece
-  __shared__ __align__(16) uint32_t s_v[TT * kVStride<D> / 4];
-  __shared__ __align__(16) uint4 s_piece[kPieces * D];
+  static_assert(kLanes >= 2 * NR, "a lane for each row's parameters");
+  __shared__ __align__(16) uint32_t s_va[G::kTiles * G::kVWords];
+  __shared__ __align__(16) uint4 s_pa[G::kTiles * kPieces * D];
   pdl_wait();
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int L = __ldcg(p.lens + b);
@@ -254,122 +266,125 @@ __global__ void __launch_bounds__(kKvqThreads, sizeof(T) == 2 ? 8 : 4) kvq_store
     end = first + p.n;
     bad = L < 0 || first < 0 || end < 1 || end > p.max_pages * P;
   }
-  if (bad) {
-    if (tid == 0 && h == 0 && blockIdx.x == 0) flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
-  } else {
-    const int tile = first / TT + blockIdx.x;
-    const int base = tile * TT;                          // first position of the tile
-    if (base < end && first < end) {
-      const int page = base / P, in_page = base - page * P;
-      const int phys = p.block_table[(size_t)b * p.max_pages + page];
-      bool ok = phys >= 0 && phys < p.num_pages_total;
-      int src = 0;
-      if (PACK) {
-        src = p.src_table[(size_t)b * p.src_max_pages + page];
-        ok = ok && src >= 0 && src < p.src_pages_total;
+  if (bad && tid == 0 && h == 0 && blockIdx.x == 0) flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
+  // this thread's tile; a tile without work still takes part in the barriers
+  const int sub = tid / kT, tt = tid % kT;
+  uint32_t* const s_v = s_va + sub * G::kVWords;
+  uint4* const s_piece = s_pa + sub * (kPieces * D);
+  const int base = (first / TT + (int)blockIdx.x * G::kTiles + sub) * TT;   // first position of the tile
+  bool work = !bad && base < end && first < end;
+  const int page = base / P, in_page = base - page * P;
+  int phys = -1, src = 0;
+  if (work) {
+    phys = p.block_table[(size_t)b * p.max_pages + page];
+    bool ok = phys >= 0 && phys < p.num_pages_total;
+    if (PACK) {
+      src = p.src_table[(size_t)b * p.src_max_pages + page];
+      ok = ok && src >= 0 && src < p.src_pages_total;
+    }
+    if (!ok) {
+      if (tt == 0) flag_status(p.status, S3R_DEV_BAD_PAGE_ID);
+      work = false;
+    }
+  }
+  if (G::kTiles == 1 ? work : __syncthreads_or(work)) {
+    uint8_t* const pg = p.pages + ((size_t)max(phys, 0) * p.Hkv + h) * Y.page_bytes;
+    const int row0 = tt / kLanes, c8 = tt % kLanes;
+    const int t0 = work ? max(first - base, 0) : 0, t1 = work ? min(end - base, TT) : 0;   // tokens of the tile written
+    Raw8<T> xk[NR], xv[NR];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      const int t = row0 + k * kRowsPass;
+      xk[k].zero();
+      xv[k].zero();
+      if (t >= t0 && t < t1) {
+        const size_t at = PACK ? (((size_t)src * p.Hkv + h) * P + in_page + t) * D + c8 * 8
+                               : (((size_t)b * p.n + (base + t - first)) * p.Hkv + h) * D + c8 * 8;
+        xk[k].load(static_cast<const T*>(p.k_src) + at);
+        xv[k].load(static_cast<const T*>(p.v_src) + at);
       }
-      if (!ok) {
-        if (tid == 0) flag_status(p.status, S3R_DEV_BAD_PAGE_ID);
+    }
+    // ranges of the 2 NR rows; then lane i of each row group works out the
+    // parameters of its i-th row, so that they cost one row's instructions
+    float mn = 0.f, mx = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2 * NR; ++k) {
+      float a, e;
+      row_range<kLanes>(k < NR ? xk[k] : xv[k - NR], &a, &e);
+      if ((c8 & 7) == k) {
+        mn = a;
+        mx = e;
+      }
+    }
+    const KvqRow row = kvq_row<BITS>(mn, mx);
+    const int group = (tid & 31) & ~(kLanes - 1);
+#pragma unroll
+    for (int k = 0; k < 2 * NR; ++k) {
+      const int t = row0 + (k % NR) * kRowsPass;
+      const bool live = t >= t0 && t < t1;
+      const float z = __shfl_sync(0xffffffffu, row.z, group + k), s = __shfl_sync(0xffffffffu, row.wide ? -row.s : row.s, group + k);
+      const float inv = __shfl_sync(0xffffffffu, row.inv, group + k);
+      uint32_t code[2], packed = 0u;
+      quantise8<T, BITS>(k < NR ? xk[k] : xv[k - NR], z, s, inv, code, &packed);
+      if (live && c8 == 0)
+        *reinterpret_cast<uint32_t*>(pg + (k < NR ? Y.off_kp : Y.off_vp) + (in_page + t) * 4) = pack_bf16x2(fabsf(s), z);
+      if (k >= NR) {
+        s_v[(t * kVStride<D>) / 4 + c8 * 2] = code[0];
+        s_v[(t * kVStride<D>) / 4 + c8 * 2 + 1] = code[1];
+      } else if (live) {
+        if (BITS == 4)
+          *reinterpret_cast<uint32_t*>(pg + ((c8 >> 2) * P + in_page + t) * 16 + (c8 & 3) * 4) = packed;
+        else
+          *reinterpret_cast<uint2*>(pg + ((c8 >> 1) * P + in_page + t) * 16 + (c8 & 1) * 8) = make_uint2(code[0], code[1]);
+      }
+    }
+    __syncthreads();
+    // four channels x eight tokens per step: lanes take 8 channel groups x 4 token groups
+    constexpr int kTg = G::kTg;
+    for (int s = tt; s < (D / 4) * kTg; s += kT) {
+      const int in = s % (8 * kTg), cg = (s / (8 * kTg)) * 8 + (in & 7), tg = in >> 3;
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = s_v[((tg * 8 + k) * kVStride<D>) / 4 + cg];
+      uint32_t a[4], o[4];
+      if (BITS == 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = w[2 * k] | (w[2 * k + 1] << 4);
+        transpose4(a, o);
+        const int piece = tg * 8 / Y.ut, word = (tg * 8 % Y.ut) / 8;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          reinterpret_cast<uint32_t*>(&s_piece[piece * D + v_slot(cg * 4 + c)])[word] = o[c];
       } else {
-        uint8_t* pg = p.pages + ((size_t)phys * p.Hkv + h) * Y.page_bytes;
-        const int row0 = tid / kLanes, c8 = tid % kLanes;
-        const int t0 = max(first - base, 0), t1 = min(end - base, TT);   // tokens of the tile written
-        Raw8<T> xk[NR], xv[NR];
 #pragma unroll
-        for (int k = 0; k < NR; ++k) {
-          const int t = row0 + k * kRowsPass;
-          xk[k].zero();
-          xv[k].zero();
-          if (t >= t0 && t < t1) {
-            const size_t at = PACK ? (((size_t)src * p.Hkv + h) * P + in_page + t) * D + c8 * 8
-                                   : (((size_t)b * p.n + (base + t - first)) * p.Hkv + h) * D + c8 * 8;
-            xk[k].load(static_cast<const T*>(p.k_src) + at);
-            xv[k].load(static_cast<const T*>(p.v_src) + at);
-          }
-        }
-        // ranges of the 2 NR rows; then lane i of each row group works out the
-        // parameters of its i-th row, so that they cost one row's instructions
-        float mn = 0.f, mx = 0.f;
+        for (int q = 0; q < 2; ++q) {
+          transpose4(w + 4 * q, o);
+          const int t = tg * 8 + 4 * q;
+          const int piece = t / Y.ut, word = (t % Y.ut) / 4;
 #pragma unroll
-        for (int k = 0; k < 2 * NR; ++k) {
-          float a, e;
-          row_range<kLanes>(k < NR ? xk[k] : xv[k - NR], &a, &e);
-          if ((c8 & 7) == k) {
-            mn = a;
-            mx = e;
-          }
-        }
-        const KvqRow row = kvq_row<BITS>(mn, mx);
-        const int group = (tid & 31) & ~(kLanes - 1);
-#pragma unroll
-        for (int k = 0; k < 2 * NR; ++k) {
-          const int t = row0 + (k % NR) * kRowsPass;
-          const bool live = t >= t0 && t < t1;
-          const float z = __shfl_sync(0xffffffffu, row.z, group + k), s = __shfl_sync(0xffffffffu, row.wide ? -row.s : row.s, group + k);
-          const float inv = __shfl_sync(0xffffffffu, row.inv, group + k);
-          uint32_t code[2], packed = 0u;
-          quantise8<T, BITS>(k < NR ? xk[k] : xv[k - NR], z, s, inv, code, &packed);
-          if (live && c8 == 0)
-            *reinterpret_cast<uint32_t*>(pg + (k < NR ? Y.off_kp : Y.off_vp) + (in_page + t) * 4) = pack_bf16x2(fabsf(s), z);
-          if (k >= NR) {
-            s_v[(t * kVStride<D>) / 4 + c8 * 2] = code[0];
-            s_v[(t * kVStride<D>) / 4 + c8 * 2 + 1] = code[1];
-          } else if (live) {
-            if (BITS == 4)
-              *reinterpret_cast<uint32_t*>(pg + ((c8 >> 2) * P + in_page + t) * 16 + (c8 & 3) * 4) = packed;
-            else
-              *reinterpret_cast<uint2*>(pg + ((c8 >> 1) * P + in_page + t) * 16 + (c8 & 1) * 8) = make_uint2(code[0], code[1]);
-          }
-        }
-        __syncthreads();
-        // four channels x eight tokens per step: lanes take 8 channel groups x 4 token groups
-        constexpr int kTg = TT / 8;
-        for (int s = tid; s < (D / 4) * kTg; s += kKvqThreads) {
-          const int in = s % (8 * kTg), cg = (s / (8 * kTg)) * 8 + (in & 7), tg = in >> 3;
-          uint32_t w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] = s_v[((tg * 8 + k) * kVStride<D>) / 4 + cg];
-          uint32_t a[4], o[4];
-          if (BITS == 4) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a[k] = w[2 * k] | (w[2 * k + 1] << 4);
-            transpose4(a, o);
-            const int piece = tg * 8 / Y.ut, word = (tg * 8 % Y.ut) / 8;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              reinterpret_cast<uint32_t*>(&s_piece[piece * D + v_slot(cg * 4 + c)])[word] = o[c];
-          } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              transpose4(w + 4 * q, o);
-              const int t = tg * 8 + 4 * q;
-              const int piece = t / Y.ut, word = (t % Y.ut) / 4;
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                reinterpret_cast<uint32_t*>(&s_piece[piece * D + v_slot(cg * 4 + c)])[word] = o[c];
-            }
-          }
-        }
-        __syncthreads();
-        for (int s = tid; s < kPieces * D; s += kKvqThreads) {
-          const int piece = s / D, d = s - (s / D) * D;
-          const int u0 = piece * Y.ut;                   // first token of the piece, within the tile
-          const int a = t0 - u0, e = t1 - u0;
-          if (e <= 0 || a >= Y.ut) continue;
-          uint4 v = s_piece[piece * D + v_slot(d)];
-          uint8_t* dst = pg + Y.off_v + ((in_page / Y.ut + piece) * D + d) * Y.unit;
-          if (a > 0 || e < Y.ut) {                       // keep the other tokens' bits
-            uint32_t* nv = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-              const uint32_t m = token_mask<BITS>(w, a, e);
-              nv[w] = (nv[w] & m) | (reinterpret_cast<const uint32_t*>(dst)[w] & ~m);
-            }
-          }
-          if (Y.unit == 16) *reinterpret_cast<uint4*>(dst) = v;
-          else *reinterpret_cast<uint2*>(dst) = make_uint2(v.x, v.y);
+          for (int c = 0; c < 4; ++c)
+            reinterpret_cast<uint32_t*>(&s_piece[piece * D + v_slot(cg * 4 + c)])[word] = o[c];
         }
       }
+    }
+    __syncthreads();
+    for (int s = tt; s < kPieces * D; s += kT) {
+      const int piece = s / D, d = s - (s / D) * D;
+      const int u0 = piece * Y.ut;                   // first token of the piece, within the tile
+      const int a = t0 - u0, e = t1 - u0;
+      if (e <= 0 || a >= Y.ut) continue;
+      uint4 v = s_piece[piece * D + v_slot(d)];
+      uint8_t* dst = pg + Y.off_v + ((in_page / Y.ut + piece) * D + d) * Y.unit;
+      if (a > 0 || e < Y.ut) {                       // keep the other tokens' bits
+        uint32_t* nv = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          const uint32_t m = token_mask<BITS>(w, a, e);
+          nv[w] = (nv[w] & m) | (reinterpret_cast<const uint32_t*>(dst)[w] & ~m);
+        }
+      }
+      if (Y.unit == 16) *reinterpret_cast<uint4*>(dst) = v;
+      else *reinterpret_cast<uint2*>(dst) = make_uint2(v.x, v.y);
     }
   }
   if (!PACK && p.lens_out) {
@@ -387,14 +402,11 @@ __global__ void __launch_bounds__(kKvqThreads, sizeof(T) == 2 ? 8 : 4) kvq_store
 
 template <typename T, int D, int P, int BITS>
 __global__ void __launch_bounds__(kKvqThreads) kvq_read_kernel(const KvqParams p) {
-  constexpr KvqLayout Y = kvq_layout(D, P, BITS);
-  constexpr int TT = P == 64 ? 32 : 16;
-  constexpr int kLanes = D / 8;
-  constexpr int kRowsPass = kKvqThreads / kLanes;
-  constexpr int NR = TT / kRowsPass;
-  constexpr int kPieces = TT / Y.ut;
-  __shared__ __align__(16) uint32_t s_v[TT * kVStride<D> / 4];
-  __shared__ __align__(16) uint4 s_piece[kPieces * D];
+  using G = Cut<D, P, BITS>;
+  constexpr KvqLayout Y = G::Y;
+  constexpr int TT = G::TT, kLanes = G::kLanes, NR = G::NR, kT = G::kT, kRowsPass = G::kRowsPass, kPieces = G::kPieces;
+  __shared__ __align__(16) uint32_t s_va[G::kTiles * G::kVWords];
+  __shared__ __align__(16) uint4 s_pa[G::kTiles * kPieces * D];
   pdl_wait();
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int L = __ldcg(p.lens + b);
@@ -404,19 +416,27 @@ __global__ void __launch_bounds__(kKvqThreads) kvq_read_kernel(const KvqParams p
     return;
   }
   const int end = p.n < L - first ? first + p.n : L;     // rows of positions >= L are left as they are
-  const int base = (first / TT + (int)blockIdx.x) * TT;
-  if (base >= end || first >= end) return;
+  const int sub = tid / kT, tt = tid % kT;               // this thread's tile; one without work still takes part in the barriers
+  uint32_t* const s_v = s_va + sub * G::kVWords;
+  uint4* const s_piece = s_pa + sub * (kPieces * D);
+  if (first >= end) return;
+  const int base = (first / TT + (int)blockIdx.x * G::kTiles + sub) * TT;
+  bool work = base < end;
   const int page = base / P, in_page = base - page * P;
-  const int phys = p.block_table[(size_t)b * p.max_pages + page];
-  if (phys < 0 || phys >= p.num_pages_total) {
-    if (tid == 0) flag_status(p.status, S3R_DEV_BAD_PAGE_ID);
-    return;
+  int phys = -1;
+  if (work) {
+    phys = p.block_table[(size_t)b * p.max_pages + page];
+    if (phys < 0 || phys >= p.num_pages_total) {
+      if (tt == 0) flag_status(p.status, S3R_DEV_BAD_PAGE_ID);
+      work = false;
+    }
   }
-  const uint8_t* pg = p.pages + ((size_t)phys * p.Hkv + h) * Y.page_bytes;
-  const int row0 = tid / kLanes, c8 = tid % kLanes;
-  const int t0 = max(first - base, 0), t1 = min(end - base, TT);
+  if (G::kTiles == 1 ? !work : !__syncthreads_or(work)) return;
+  const uint8_t* pg = p.pages + ((size_t)max(phys, 0) * p.Hkv + h) * Y.page_bytes;
+  const int row0 = tt / kLanes, c8 = tt % kLanes;
+  const int t0 = work ? max(first - base, 0) : 0, t1 = work ? min(end - base, TT) : 0;
   // every load of the tile first
-  for (int s = tid; s < kPieces * D; s += kKvqThreads) {
+  if (work) for (int s = tt; s < kPieces * D; s += kT) {
     const int piece = s / D, d = s - (s / D) * D;
     const uint8_t* src = pg + Y.off_v + ((in_page / Y.ut + piece) * D + d) * Y.unit;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -433,6 +453,9 @@ __global__ void __launch_bounds__(kKvqThreads) kvq_read_kernel(const KvqParams p
 #pragma unroll
   for (int k = 0; k < NR; ++k) {
     const int t = in_page + row0 + k * kRowsPass;
+    kc[k] = make_uint2(0u, 0u);
+    kp[k] = vp[k] = 0u;
+    if (G::kTiles > 1 && !work) continue;
     if (BITS == 4) kc[k].x = __ldcg(reinterpret_cast<const uint32_t*>(pg + ((c8 >> 2) * P + t) * 16 + (c8 & 3) * 4));
     else kc[k] = __ldcg(reinterpret_cast<const uint2*>(pg + ((c8 >> 1) * P + t) * 16 + (c8 & 1) * 8));
     kp[k] = __ldcg(reinterpret_cast<const uint32_t*>(pg + Y.off_kp + t * 4));
@@ -461,8 +484,8 @@ __global__ void __launch_bounds__(kKvqThreads) kvq_read_kernel(const KvqParams p
     }
   }
   __syncthreads();
-  constexpr int kTg = TT / 8;
-  for (int s = tid; s < (D / 4) * kTg; s += kKvqThreads) {
+  constexpr int kTg = G::kTg;
+  for (int s = tt; s < (D / 4) * kTg; s += kT) {
     const int in = s % (8 * kTg), cg = (s / (8 * kTg)) * 8 + (in & 7), tg = in >> 3;
     uint32_t a[4], o[4];
     if (BITS == 4) {
@@ -527,10 +550,11 @@ KvqParams base_params(const s3r_paged_kvq& c, void* ws) {
   return p;
 }
 
-// Tiles of TT tokens that n consecutive positions may touch.
-int tiles_of(int n, int P) {
-  const int tt = P == 64 ? 32 : 16;
-  return n <= 0 ? 1 : (n + tt - 2) / tt + 1;
+// CTAs for the tiles that n consecutive positions may touch.
+unsigned tile_ctas(int n, int D, int P) {
+  const int tt = P == 64 ? 32 : 16, per = kKvqThreads / (tt * (D / 8) / 4);
+  const int tiles = n <= 0 ? 1 : (n + tt - 2) / tt + 1;
+  return (unsigned)((tiles + per - 1) / per);
 }
 
 enum KvqOp { kStoreRows, kStorePages, kRead };
@@ -568,7 +592,7 @@ cudaError_t launch_kvq_append(const s3r_paged_kvq& c, int32_t* lens, const void*
   p.v_src = v_new;
   p.n = n;
   p.overwrite = overwrite;
-  return launch_typed(kStoreRows, dt, c, p, dim3(tiles_of(n, c.page_size), c.num_kv_heads, c.num_seqs), st);
+  return launch_typed(kStoreRows, dt, c, p, dim3(tile_ctas(n, c.head_dim, c.page_size), c.num_kv_heads, c.num_seqs), st);
 }
 
 cudaError_t launch_kvq_pack(const s3r_paged_kv& kv, const s3r_paged_kvq& c, int32_t last_n, void* ws, cudaStream_t st) {
@@ -582,7 +606,7 @@ cudaError_t launch_kvq_pack(const s3r_paged_kv& kv, const s3r_paged_kvq& c, int3
   p.n = last_n;
   const int cap = (c.max_pages_per_seq < kv.max_pages_per_seq ? c.max_pages_per_seq : kv.max_pages_per_seq) * c.page_size;
   const int n = last_n > 0 && last_n < cap ? last_n : cap;
-  return launch_typed(kStorePages, kv.dtype, c, p, dim3(tiles_of(n, c.page_size), c.num_kv_heads, c.num_seqs), st);
+  return launch_typed(kStorePages, kv.dtype, c, p, dim3(tile_ctas(n, c.head_dim, c.page_size), c.num_kv_heads, c.num_seqs), st);
 }
 
 cudaError_t launch_kvq_read(const s3r_paged_kvq& c, const int32_t* start, int32_t n, s3r_dtype dt, void* k_out, void* v_out,
@@ -593,7 +617,7 @@ cudaError_t launch_kvq_read(const s3r_paged_kvq& c, const int32_t* start, int32_
   p.k_out = k_out;
   p.v_out = v_out;
   const int cap = c.max_pages_per_seq * c.page_size;
-  return launch_typed(kRead, dt, c, p, dim3(tiles_of(n < cap ? n : cap, c.page_size), c.num_kv_heads, c.num_seqs), st);
+  return launch_typed(kRead, dt, c, p, dim3(tile_ctas(n < cap ? n : cap, c.head_dim, c.page_size), c.num_kv_heads, c.num_seqs), st);
 }
 
 cudaError_t launch_kvq_rollback(const s3r_paged_kvq& c, int32_t* lens, const int32_t* num_accepted, int32_t rows, void* ws,
