@@ -572,7 +572,9 @@ s3r_status s3r_kvq_rollback(const s3r_paged_kvq* kvq, int32_t* context_lens, con
  * q, out: [S, rows, Hq, D] in `dtype` (f32 or bf16), 16-byte aligned; lse:
  *   float32 [S, rows, Hq] or NULL.
  * Scores, softmax sums and outputs accumulate in float32. bf16: each weight
- *   p s_v is rounded to bf16 before it meets the values' whole numbers.
+ *   p s_v is rounded once before it meets the values' whole numbers, to float16
+ *   or (4 bits, up to 16 packed rows G * rows) to 9 significant bits; held values
+ *   larger than 2^100 may overflow.
  * Supported as s3r_verify_attn: G <= 8, rows <= 17, G * rows <= 128.
  * workspace: s3r_kvq_attn_workspace_bytes(kvq, dtype, rows, budget_pages)
  *   bytes, zero-filled before first use.

@@ -10,16 +10,20 @@
 //   kvq_read_kernel      a window of positions back to rows of bf16 / f32
 //   kvq_rollback_kernel  the lengths back to the committed prefix
 //
-// All are bound by HBM at length and by a chain of dependent loads (length ->
-// page id -> rows) for single rows. A CTA of 128 threads takes one tile of T
-// consecutive tokens of one (sequence, KV head), T = 32 for 64-token pages
-// and 16 for 16-token ones: a tile then holds whole V pieces, so the V bytes
-// of a tile belong to one CTA and no two CTAs of a call write the same byte.
-// A row is D/8 lanes of 8 channels (16-byte loads of bf16); minimum and maximum meet
-// by shuffles; with small rows or pages a CTA takes two or four tiles. K numbers go out as they are; V numbers turn channel-major
-// through shared memory, four channels by eight tokens per thread with byte
-// permutes, and leave as 16-byte pieces. A V piece of which only some tokens
-// are written keeps the other tokens' bits.
+// Measured (16 x 16384 tokens, 8 KV heads, D 128, 4 bits): quantising a bf16 cache
+// 386 us, 3.5 TB/s, bound by instruction issue (77% of cycles, 20 instructions a
+// value); reading back 249 us, 5.5 TB/s, 0.83 of a copy's rate. Single rows are a
+// chain of dependent loads (length -> page id -> rows), 3 to 4 us a kernel.
+//
+// A CTA of 128 threads takes tiles of T consecutive tokens of one (sequence, KV
+// head), T = 32 for 64-token pages and 16 for 16-token ones: a tile then holds
+// whole V pieces, so the V bytes of a tile belong to one CTA and no two CTAs of
+// a call write the same byte; with small rows or pages a CTA takes two or four
+// tiles. A row is D/8 lanes of 8 channels (16-byte loads of bf16); minimum and
+// maximum meet by shuffles. K numbers go out as they are; V numbers turn
+// channel-major through shared memory, four channels by eight tokens per
+// thread with byte permutes, and leave as 16-byte pieces. A V piece of which
+// only some tokens are written keeps the other tokens' bits.
 //
 // These kernels write inputs of later calls: they wait for the previous kernel
 // before touching anything and let the next one start only when they are done.

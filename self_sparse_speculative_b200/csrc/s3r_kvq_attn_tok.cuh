@@ -2,44 +2,56 @@
 // queries, up to 64 packed rows (G query heads x R rows) per (sequence, KV
 // head). Layout and arithmetic of a held row: s3r_kvq.cuh.
 //
-// The held numbers themselves go through the tensor cores, centred (c = 8 at 4
-// bits, 128 at 8); scales and minima meet the results outside:
+// The held numbers themselves go through the tensor cores, as n - c with a
+// constant c; scales and minima meet the results outside:
 //   S^T[t, i] = sum_d (n_k[t, d] - c) q[i, d]
 //   y         = scale log2 e (s_k[t] S^T + (z_k[t] + c s_k[t]) sum_d q[i, d]),   p = 2^(y - reference)
-//   w[t, i]   = p s_v[t], w' = w rounded to float16
+//   w[t, i]   = p s_v[t], rounded to w'
 //   O^T[d, i] = sum_t (n_v[t, d] - c) w'[t, i]
 //   out       = (O^T + sum_t w (z_v[t] / s_v[t] + c)) / sum_t p
-// float16 holds the centred numbers exactly and a weight to 2^-12 of itself;
-// the rounding of w meets only the centred numbers, the rows' means are summed
-// with the unrounded weight, and sums over tokens stay near zero (with n
-// itself the accumulator's truncation built up an error of 1e-2 over 16384
-// tokens). The reference of a row bounds y + log2 s_v, so that w stays in
-// float16's range whatever the values' scales; a bf16 query row is met as q 2^e
-// with a power-of-two scale per row (exact down to 2^-21 of the row's largest).
+// The reference of a row bounds y + log2 s_v, so that w stays in a narrow
+// type's range whatever the values' scales; queries are met as q 2^e with a
+// power of two per row. Sums over tokens stay near zero (with n itself, or 16
+// + n, the accumulator's truncation built up an error of 1e-2 over 16384 tokens).
 //
-// Unpacking: a number placed in the mantissa of 1024 (or 16 times it, in place,
-// for the odd half-bytes) by one logic operation for two numbers, centred by
-// one fused multiply-add on the other pipe. Logic operations issue at half
-// rate, and they bound the unpacking: 5 of them for eight 4-bit numbers, 4 for
-// eight 8-bit ones. (bf16 has 7 mantissa bits and needs a shift each: 8. e4m3
-// needs 3, but two terms for queries and weights: measured 97 us against ... )
+// Two forms of the numbers:
+// - f16, c = 8 or 128 (8 bits; 4 bits beyond 16 rows): a number placed in the
+//   mantissa of 1024 (or 16 times it, in place, for the odd half-bytes) by one
+//   logic operation for two, centred by one fused multiply-add: 9 instructions
+//   for eight 4-bit numbers, 8 for eight 8-bit ones. Queries and weights are one f16
+//   term (w to 2^-12 of itself, a bf16 query exactly down to 2^-21 of its row's largest).
+// - e4m3, c = 0 (4 bits, up to 16 rows): a 4-bit number in the low bits of a
+//   byte is, read as e4m3, exactly n 2^-9 (subnormals and the first binade have
+//   one spacing): 3 instructions for eight. Queries and weights are two terms hi +
+//   lo / 32 in separate columns, w rounded to 9 bits once for both its sums.
+//   Every other token's numbers are complemented (15 - n) and its weights
+//   negated, which keeps the sums over tokens near zero. The two terms cost the
+//   softmax 7 instructions a row and token: measured over 64 x 8192 tokens, 4
+//   rows take 572 ns a stage against 949 in f16, 8 rows 707 against 991, 16 rows 990
+//   against 1089; 24 rows were slower in it (1448 against 1385 ns, an earlier state of both).
 //
 // Both operands of numbers are the MMA's A operand (M = 128 tokens of S^T, M =
 // 128 lanes of channels of O^T) and live in tensor memory: a thread unpacks
 // one token's channels (one channel's tokens) from 16-byte shared-memory reads
-// into registers and stores them to its TMEM lane, so the unpacked form, 4
+// into registers and stores them to its TMEM lane, so the unpacked form, 2 to 4
 // times the packed bytes, never crosses shared memory. Q and w are the B
 // operands in shared memory.
 //
-// Warps: two softmax warpgroups (thread = token), two unpacking ones (on
-// alternate stages), one producer (a bulk copy per (page, head) into an NS-stage ring of
-// 128 tokens), one MMA issuer per product. A stage's softmax is a chain of
-// waits and latencies of about 1500 cycles, twice what a stage's bytes take, so
-// up to 24 rows the warpgroups take alternate stages (ALT): each keeps its own
-// references, sums and O^T, merged at the end of a segment. More rows do not
-// fit a thread's registers: there the warpgroups share the rows of every stage. Work is split over
-// CTAs as in the bf16 attention (s3r_attn_sched.cuh), units shared by several
-// CTAs merge by log-sum-exp in the last one to finish.
+// Warps: two softmax warpgroups (thread = token), two unpacking ones, one
+// producer (a bulk copy per (page, head) into a ring of 128-token stages), one
+// MMA issuer per product. Up to 24 rows the softmax warpgroups take alternate
+// stages (ALT): a stage's softmax is a chain of waits and latencies of about
+// 1500 cycles, twice what a stage's bytes take; each keeps its own references,
+// sums and O^T, merged at the end of a segment. More rows do not fit a thread's
+// registers: there the warpgroups share the rows of every stage. Work is split
+// over CTAs as in the bf16 attention (s3r_attn_sched.cuh), units shared by
+// several CTAs merge by log-sum-exp in the last one to finish.
+//
+// What bounds it, measured: HBM for few rows in 8 bits (64 x 8192 tokens, 8 KV heads, 1
+// to 4 rows: 6.3 TB/s, 0.96 of a copy's rate). Elsewhere instruction issue: five roles share
+// every SM quadrant, about 570 instructions a stage at 4 rows and 4 bits, issued in 53%
+// of cycles with instruction fetch among the first stalls (4.5 TB/s, 0.69;
+// 16 x 16384 tokens 67 us a call, 285 MB). 45 rows: 256 x 8192 tokens 1285 us, 1.8 TB/s.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -62,7 +74,7 @@ constexpr int kTok = 128;                    // tokens per stage
 constexpr int kHidden = 0x7fffffff;
 constexpr float kNuInit = 1e30f;             // -(reference) before the first score of a segment
 constexpr int kSmemBudget = 232448 - 10240;  // beside the static arrays
-constexpr int kMaxPend = 8;                  // deferred merges of units per CTA
+constexpr int kMaxPend = 2;                  // units a CTA's range shares with others: its first and its last
 constexpr int kThreads = 608;                // 8 softmax and 8 unpacking warps, producer, two MMA issuers
 constexpr int kSoft = 256;                   // softmax threads
 constexpr int kProducer = 16, kMmaQk = 17, kMmaPv = 18;
@@ -376,7 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   __shared__ __align__(8) uint64_t s_bar[2 * NS + 3 * NB + NKE + kNT + NSB + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int s_ticket;
   __shared__ int4 s_pend[kMaxPend];                      // units this CTA merges at its end: (b, h, slot0, nseg)
   __shared__ int s_npend;
   __shared__ int s_prefix[kMaxSeqs + 1];
@@ -1098,21 +1109,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           sync_wg(wg);
           if (tid == 0) {
             __threadfence();
-            s_ticket = atomicAdd(p.tickets + sg.unit, 1u);
-          }
-          sync_wg(wg);
-          if (s_ticket == sg.nseg - 1) {
-            // this CTA finished the unit last: merge its partials after the
-            // CTA's own streaming is done (immediately if the list is full)
-            if (s_npend < kMaxPend) {
-              if (tid == 0) s_pend[s_npend] = make_int4(sg.b, sg.h, sg.first_cta + sg.unit, sg.nseg);
-            } else {
-              __threadfence();
-              kvq_combine<__nv_bfloat16>(p, sg.b, sg.h, sg.first_cta + sg.unit, sg.nseg, 128);
-            }
-            sync_wg(wg);
-            if (tid == 0) {
-              if (s_npend < kMaxPend) ++s_npend;
+            if (atomicAdd(p.tickets + sg.unit, 1u) == (unsigned)(sg.nseg - 1)) {
+              // this CTA finished the unit last: its partials are merged after
+              // the CTA's own streaming is done
+              s_pend[s_npend++] = make_int4(sg.b, sg.h, sg.first_cta + sg.unit, sg.nseg);
               p.tickets[sg.unit] = 0u;
             }
           }

@@ -12,9 +12,9 @@ N = 2^bits - 1, c = N / 2, T tokens):
   each of D values off by at most 2^-32 of the row's largest, times scale s_k N.
   With the base-2 exponential's 2^-21 relative error a weight is off by e + 2^-21 +
   4 u |score| of itself, which moves the output by at most twice that times A;
-- bf16, 8 bits or more than 24 packed rows: a weight w = p s_v is rounded to float16: off by at most 2^-12 w + 2^-25,
+- bf16, 8 bits or more than 16 packed rows: a weight w = p s_v is rounded to float16: off by at most 2^-12 w + 2^-25,
   where the row's largest weight is at least 2^8; the error meets n - c, at most c + 1 in size: (c + 1) (2^-12 B + T
-  2^-33 max s_v). 4 bits, up to 24 packed rows: w is rounded to 9 bits, which moves the
+  2^-33 max s_v). 4 bits, up to 16 packed rows: w is rounded to 9 bits, which moves the
   output by at most 2^-9 A, and held in two e4m3 terms, off by at most 2^-15 where the row's largest is at
   least 2^6, which meets n: N T 2^-21 max s_v; a query's two terms leave at most 2^-15 of a value where the row's
   largest is at least 128: D values of 2^-22 of the row's largest, times scale s_k N. The output's rounding is 2^-8 |out|;
@@ -94,7 +94,7 @@ class Case:
             sumq = np.abs(q.astype(np.float64)).sum(-1)                         # [R, Hq]
             span = (held["sk"] * (N + 1) + np.abs(held["zk"])).max(0).repeat(self.G)   # [Hq]
             e = (32 + self.D / 4) * U * self.scale * span * sumq
-            e4 = self.dtype == "bf16" and self.bits == 4 and self.G * self.rows <= 24
+            e4 = self.dtype == "bf16" and self.bits == 4 and self.G * self.rows <= 16
             if self.dtype == "bf16":
                 e = e + (self.D * 2.0 ** (-22 if e4 else -32) * np.abs(q).max(-1) * self.scale * N
                          * held["sk"].max(0).repeat(self.G))
