@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kKvqThreads) kvq_rollback_kernel(const KvqPara
   if (b >= p.S) return;
   const int L = p.lens_out[b], nacc = p.num_accepted[b];
   const int new_len = L - p.rows + nacc + 1;
-  if (nacc < 0 || nacc >= p.rows || new_len < 1 || L > p.max_pages * p.P) {
+  if (nacc < 0 || nacc >= p.rows || L < 1 || new_len < 1 || L > p.max_pages * p.P) {
     flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
     return;
   }

@@ -251,3 +251,12 @@ def test_bf16_values_far_apart_in_size(bits):
     Q.append(pages, table, [0], x.reshape(1, n, H, D), x.reshape(1, n, H, D), bits, P, 0)
     assert np.array_equal(dev["pages"].cpu().numpy(), pages)
     ok(dev)
+
+
+def test_rollback_of_the_lowest_length_is_refused():
+    lens = [-2 ** 31, -2 ** 31 + 2, 1, 7]
+    _, _, dev = cache(4, 1, 64, 16, 4, lens, 1, seed=3)
+    acc = torch.tensor([0, 0, 3, 0], dtype=torch.int32, device="cuda")
+    s3r.s3r_kvq_rollback(dev["kvq"], dev["lens"], acc, 4, dev["ws"])
+    assert dev["lens"].tolist() == [-2 ** 31, -2 ** 31 + 2, 1, 4]
+    assert s3r.s3r_device_status(dev["ws"])[1] == s3r.S3R_DEV_BAD_CONTEXT_LEN
