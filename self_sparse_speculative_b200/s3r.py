@@ -343,6 +343,14 @@ def _kvq_env(dtype):
     return device, _torch.bfloat16 if code == S3R_BF16 else _torch.float32, code
 
 
+def _same_device(device, kvq, workspace):
+    """Refuses a cache or a workspace of another device: the launch goes to the current one."""
+    if getattr(kvq, "device", device) != device:
+        raise ValueError(f"the quantised cache lives on cuda:{kvq.device}, the current device is cuda:{device}")
+    if hasattr(workspace, "get_device") and workspace.get_device() != device:
+        raise ValueError(f"workspace lives on {workspace.device}, the current device is cuda:{device}")
+
+
 def _stream_on(stream, device):
     """_stream(stream), without building a stream object for the current one (3 us of a small call)."""
     if stream is None and device >= 0:
@@ -365,6 +373,7 @@ def paged_kvq(pages, block_table, context_lens, num_q_heads: int, head_dim: int,
     kvq = PagedKVQ(int(block_table.shape[0]), int(num_q_heads), int(h), int(head_dim), int(page_size),
                    int(block_table.shape[1]), int(n), int(bits), _ptr(pages), _ptr(block_table), _ptr(context_lens))
     kvq.tensors = (pages, block_table, context_lens)     # alive as long as the description
+    kvq.device = device
     return kvq
 
 
@@ -375,6 +384,7 @@ def s3r_kvq_append(kvq: PagedKVQ, context_lens, k_new, v_new, dtype, n: int, ove
     device, dt, code = _kvq_env(dtype)
     shape = (kvq.num_seqs, n, kvq.num_kv_heads, kvq.head_dim)
     _expect(device, ("k_new", k_new, dt, shape), ("v_new", v_new, dt, shape))
+    _same_device(device, kvq, workspace)
     st = _lib.s3r_kvq_append(ctypes.byref(kvq), _ptr(context_lens), _ptr(k_new), _ptr(v_new), code, int(n),
                              int(overwrite), _ptr(workspace), wb, _stream_on(stream, device))
     _check("s3r_kvq_append", st)
@@ -384,6 +394,7 @@ def s3r_kvq_pack(kv: PagedKV, kvq: PagedKVQ, last_n: int, workspace, workspace_b
     """Quantise the last last_n positions (0: all) of each sequence of kv into kvq."""
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
     device, _, _ = _kvq_env(None)
+    _same_device(device, kvq, workspace)
     st = _lib.s3r_kvq_pack(ctypes.byref(kv), ctypes.byref(kvq), int(last_n), _ptr(workspace), wb, _stream_on(stream, device))
     _check("s3r_kvq_pack", st)
 
@@ -394,6 +405,7 @@ def s3r_kvq_read(kvq: PagedKVQ, start, n: int, dtype, k_out, v_out, workspace, w
     device, dt, code = _kvq_env(dtype)
     shape = (kvq.num_seqs, n, kvq.num_kv_heads, kvq.head_dim)
     _expect(device, ("start", start, _torch.int32, (kvq.num_seqs,)), ("k_out", k_out, dt, shape), ("v_out", v_out, dt, shape))
+    _same_device(device, kvq, workspace)
     st = _lib.s3r_kvq_read(ctypes.byref(kvq), _ptr(start), int(n), code, _ptr(k_out), _ptr(v_out),
                            _ptr(workspace), wb, _stream_on(stream, device))
     _check("s3r_kvq_read", st)
@@ -404,6 +416,7 @@ def s3r_kvq_rollback(kvq: PagedKVQ, context_lens, num_accepted, rows: int, works
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
     device, _, _ = _kvq_env(None)
     _expect(device, ("num_accepted", num_accepted, _torch.int32, (kvq.num_seqs,)))
+    _same_device(device, kvq, workspace)
     st = _lib.s3r_kvq_rollback(ctypes.byref(kvq), _ptr(context_lens), _ptr(num_accepted), int(rows), _ptr(workspace), wb,
                                _stream_on(stream, device))
     _check("s3r_kvq_rollback", st)
@@ -421,6 +434,7 @@ def s3r_kvq_attn(kvq: PagedKVQ, q, dtype, rows: int, scale: float, out, lse, wor
     shape = (kvq.num_seqs, rows, kvq.num_q_heads, kvq.head_dim)
     _expect(device, ("q", q, dt, shape), ("out", out, dt, shape), ("lse", lse, _torch.float32, shape[:3]),
             ("pages", pages, _torch.int32, (kvq.num_seqs, kvq.num_kv_heads, budget_pages)))
+    _same_device(device, kvq, workspace)
     st = _lib.s3r_kvq_attn(ctypes.byref(kvq), _ptr(q), code, int(rows), _ptr(pages), int(budget_pages),
                            float(scale), _ptr(out), _ptr(lse), _ptr(workspace), wb, _stream_on(stream, device))
     _check("s3r_kvq_attn", st)

@@ -132,3 +132,29 @@ def test_binding_refuses_tensors_of_other_shapes_and_places():
     with pytest.raises(ValueError, match="pages"):
         s3r.s3r_kvq_attn(c, FAKE, "bf16", 1, 0.1, FAKE, None, ws, pages=torch.zeros((2, 2, 3), dtype=torch.int32),
                          budget_pages=4, stream=0)
+
+
+class _Elsewhere:
+    """A workspace of another device."""
+    device = "cuda:5"
+    numel = lambda self: 1 << 20           # noqa: E731
+    element_size = lambda self: 1          # noqa: E731
+    get_device = lambda self: 5            # noqa: E731
+    data_ptr = lambda self: FAKE           # noqa: E731
+
+
+@pytest.mark.parametrize("what", ["cache", "workspace"])
+def test_binding_refuses_a_cache_or_workspace_of_another_device(what):
+    c, ws, match = _kvq(), torch.zeros(4096, dtype=torch.uint8), "quantised cache lives on cuda:5"
+    if what == "cache":
+        c.device = 5
+    else:
+        ws, match = _Elsewhere(), "workspace lives on cuda:5"
+    calls = [lambda: s3r.s3r_kvq_append(c, FAKE, FAKE, FAKE, "bf16", 1, 0, ws, stream=0),
+             lambda: s3r.s3r_kvq_pack(_kv(), c, 0, ws, stream=0),
+             lambda: s3r.s3r_kvq_read(c, None, 1, "bf16", FAKE, FAKE, ws, stream=0),
+             lambda: s3r.s3r_kvq_rollback(c, FAKE, FAKE, 1, ws, stream=0),
+             lambda: s3r.s3r_kvq_attn(c, FAKE, "bf16", 1, 0.1, FAKE, None, ws, stream=0)]
+    for call in calls:
+        with pytest.raises(ValueError, match=match):
+            call()
