@@ -309,6 +309,41 @@ def test_without_lse_on_another_stream_and_repeatable():
     assert torch.equal(c.out, ref) and torch.equal(c.lse, lse)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+def test_other_scales(scale, bits, dtype):
+    c = Case(2, 2, 4, 128, 64, bits, [333, 5], 2, dtype, seed=21)
+    c.scale = scale
+    c.call()
+    if scale >= 0:
+        c.check()
+    else:                                                                      # the same rows, queries negated
+        out, lse = c.out.clone(), c.lse.clone()
+        c.scale, c.q = -scale, -c.q
+        c.check()
+        c.call()
+        assert torch.equal(out, c.out) and torch.equal(lse, c.lse)
+    c.ok()
+
+
+@pytest.mark.parametrize("bits,G,rows,dtype", [(4, 4, 2, "bf16"), (4, 4, 5, "bf16"), (8, 4, 2, "bf16"), (8, 5, 9, "bf16"),
+                                               (4, 4, 2, "f32")])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_queries_that_are_not_finite_reach_their_own_row_only(bits, G, rows, dtype, value):
+    c = Case(2, 2, G, 128, 64, bits, [700, 130], rows, dtype, seed=22)
+    c.call()
+    out, lse, q = c.out.clone(), c.lse.clone(), c.q.clone()
+    at = (0, rows - 1, G)
+    c.q[at][17] = value
+    c.call()
+    c.ok()
+    if value != value:
+        assert c.out[at].isnan().all() and c.lse[at].isnan()
+    c.out[at], c.lse[at], c.q = out[at], lse[at], q
+    c.check()
+
+
 def test_captured_graphs_share_a_workspace():
     # two graphs over one workspace, replayed one after the other, in both orders
     c = Case(2, 2, 4, 128, 64, 8, [3000, 700], 2, "bf16", seed=11)
