@@ -27,7 +27,7 @@
 //   Every other token's numbers are complemented (15 - n) and its weights
 //   negated, which keeps the sums over tokens near zero. The two terms cost the
 //   softmax 7 instructions a row and token: measured over 64 x 8192 tokens, 4
-//   rows take 572 ns a stage against 949 in f16, 8 rows 707 against 991, 16 rows 990
+//   rows take 568 ns a stage against 949 in f16, 8 rows 685 against 991, 16 rows 953
 //   against 1089; 24 rows were slower in it (1448 against 1385 ns, an earlier state of both).
 //
 // Both operands of numbers are the MMA's A operand (M = 128 tokens of S^T, M =
@@ -51,7 +51,9 @@
 // to 4 rows: 6.3 TB/s, 0.96 of a copy's rate). Elsewhere instruction issue: five roles share
 // every SM quadrant, about 570 instructions a stage at 4 rows and 4 bits, issued in 53%
 // of cycles with instruction fetch among the first stalls (4.5 TB/s, 0.69;
-// 16 x 16384 tokens 67 us a call, 285 MB). 45 rows: 256 x 8192 tokens 1285 us, 1.8 TB/s.
+// 16 x 16384 tokens 67 us a call, 285 MB). 45 rows: 256 x 8192 tokens 1245 us, 1.9 TB/s: a
+// stage of the softmax warpgroups takes about 2300 cycles, 1300 of them scores and
+// weights, the rest the latencies of three waits, parameters and a barrier.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -313,6 +315,13 @@ __device__ __forceinline__ void warp_part(float* v, float (*red)[32], int q4, in
 }
 
 // Barrier over a softmax warpgroup (barriers 1 and 2).
+// Whether the phase of the given parity is complete, without suspending.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r) : "r"(bar), "r"(parity) : "memory");
+  return r != 0u;
+}
 __device__ __forceinline__ void sync_wg(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
 // Number of its threads whose predicate is true.
 __device__ __forceinline__ int count_wg(int wg, bool pred) {
@@ -838,6 +847,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       for (; g < g0 + nst; ++g) {
         if (ALT && (int)(g & 1) != wg) continue;
         const uint32_t sb = g & 1;
+        // The products' barriers are asked early, so that the answers' latency
+        // passes under other work: with shared rows both before the parameters (48
+        // rows: 1575 -> 1520 ns a stage); with alternate stages only PV(g - 2)'s, and
+        // later, when it is likely done (8 rows 706 -> 685, at the top 718).
+        auto o_test = [&]() { return g < 2 || mbar_test(BAR(B_VE + (g - 2) % NB), ((g - 2) / NB) & 1); };
+        bool s_early = false, o_early = false;
+        if (!ALT) {
+          s_early = mbar_test(BAR(B_KE + g % NKE), (g / NKE) & 1);
+          o_early = o_test();
+        }
         ok &= mbar_wait(BAR(B_TF + g % kNT), (g / kNT) & 1, &s_abort, p.status);
         const uint8_t* const tp = dyn + L::kOffT + (g % kNT) * (128 * 24);
         const float4 ta = reinterpret_cast<const float4*>(tp)[t];
@@ -857,7 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           lgs = zc = 0.f;
           rsv = 1.f;
         }
-        ok &= s_done(g);
+        if (ALT) o_early = o_test();
+        if (!s_early) ok &= s_done(g);
         tc_fence_after();
         float s[NR];
         // s <- y + log2 s_v (- reference); hidden: -inf
@@ -941,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         // w buffer sb was last read by PV(g - 2); a rescale of O^T also needs
         // its last PV done (ALT: the same)
         const uint32_t back = !ALT && rescale_o ? 1 : 2;
-        if (g >= back) ok &= o_done(g - back);
+        if (back == 1 ? g >= 1 : !o_early) ok &= o_done(g - back);
         tc_fence_after();
         if (rescale_o) {
 #pragma unroll
