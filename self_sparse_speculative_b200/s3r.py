@@ -315,6 +315,7 @@ def s3r_kvq_page_bytes(head_dim: int, page_size: int, bits: int) -> int:
 
 
 _torch = None
+_kvq_types = {}                  # name of a type -> (torch type, code)
 
 
 def _expect(device, *args):
@@ -326,9 +327,10 @@ def _expect(device, *args):
         if x.shape != shape or x.dtype != dtype or not x.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                              f"got {x.dtype} {tuple(x.shape)}")
-        if not x.is_cuda:
+        at = x.get_device()                                  # -1 on the host
+        if at < 0:
             raise ValueError(f"{name} must live on the GPU")
-        if x.get_device() != device:
+        if at != device:
             raise ValueError(f"{name} lives on {x.device}, the current device is cuda:{device}")
 
 
@@ -338,9 +340,12 @@ def _kvq_env(dtype):
     if _torch is None:
         import torch
         _torch = torch
-    code = dtype_code(dtype) if dtype is not None else S3R_BF16
+    known = _kvq_types.get(dtype)
+    if known is None:
+        code = dtype_code(dtype) if dtype is not None else S3R_BF16
+        known = _kvq_types[dtype] = (_torch.bfloat16 if code == S3R_BF16 else _torch.float32, code)
     device = _torch.cuda.current_device() if _torch.cuda.is_initialized() else -1
-    return device, _torch.bfloat16 if code == S3R_BF16 else _torch.float32, code
+    return device, known[0], known[1]
 
 
 def _same_device(device, kvq, workspace):
