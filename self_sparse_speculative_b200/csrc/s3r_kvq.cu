@@ -82,22 +82,21 @@ template <> struct Raw8<float> {
   }
 };
 
-// Minimum and maximum over a row (kLanes lanes), NaN if it holds one. bf16:
-// exact in packed bf16, both in one word {min, -max} across the lanes.
+// Minimum and maximum over a row, NaN if it holds one. bf16: exact in packed
+// bf16, both in one word {min, -max} across the lanes.
 __device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
-template <int kLanes>
-__device__ __forceinline__ void row_range(const Raw8<__nv_bfloat16>& x, float* mn, float* mx) {
+__device__ __forceinline__ uint32_t range_of(const Raw8<__nv_bfloat16>& x) {
   const uint32_t lo = as_u32(__hmin2_nan(__hmin2_nan(as_bf2(x.w[0]), as_bf2(x.w[1])), __hmin2_nan(as_bf2(x.w[2]), as_bf2(x.w[3]))));
   const uint32_t hi = as_u32(__hmax2_nan(__hmax2_nan(as_bf2(x.w[0]), as_bf2(x.w[1])), __hmax2_nan(as_bf2(x.w[2]), as_bf2(x.w[3]))));
-  uint32_t m = as_u32(__hmin2_nan(as_bf2(__byte_perm(lo, hi ^ 0x80008000u, 0x5410)), as_bf2(__byte_perm(lo, hi ^ 0x80008000u, 0x7632))));
-#pragma unroll
-  for (int o = kLanes / 2; o >= 1; o >>= 1) m = as_u32(__hmin2_nan(as_bf2(m), as_bf2(__shfl_xor_sync(0xffffffffu, m, o))));
-  *mn = __uint_as_float(m << 16);
-  *mx = __uint_as_float((m & 0xffff0000u) ^ 0x80000000u);
+  return as_u32(__hmin2_nan(as_bf2(__byte_perm(lo, hi ^ 0x80008000u, 0x5410)), as_bf2(__byte_perm(lo, hi ^ 0x80008000u, 0x7632))));
 }
-template <int kLanes>
-__device__ __forceinline__ void row_range(const Raw8<float>& x, float* mn, float* mx) {
+__device__ __forceinline__ uint32_t range_join(uint32_t a, uint32_t b) { return as_u32(__hmin2_nan(as_bf2(a), as_bf2(b))); }
+__device__ __forceinline__ uint32_t range_from(uint32_t a, int lanes) { return __shfl_xor_sync(0xffffffffu, a, lanes); }
+__device__ __forceinline__ float2 range_ends(uint32_t m) {
+  return make_float2(__uint_as_float(m << 16), __uint_as_float((m & 0xffff0000u) ^ 0x80000000u));
+}
+__device__ __forceinline__ float2 range_of(const Raw8<float>& x) {
   float a = x.a.x, b = x.a.x;
   const float y[7] = {x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
 #pragma unroll
@@ -105,13 +104,30 @@ __device__ __forceinline__ void row_range(const Raw8<float>& x, float* mn, float
     a = min_nan(a, y[i]);
     b = max_nan(b, y[i]);
   }
+  return make_float2(a, b);
+}
+__device__ __forceinline__ float2 range_join(float2 a, float2 b) { return make_float2(min_nan(a.x, b.x), max_nan(a.y, b.y)); }
+__device__ __forceinline__ float2 range_from(float2 a, int lanes) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, a.x, lanes), __shfl_xor_sync(0xffffffffu, a.y, lanes));
+}
+__device__ __forceinline__ float2 range_ends(float2 m) { return m; }
+
+// The ranges of eight rows, r[k] this lane's share of row k: lane c8 of the
+// row's kLanes gets row c8 % 8's. Lanes swap halves of the rows, then quarters,
+// then single rows: 8 shuffles instead of 32.
+template <int kLanes, typename R>
+__device__ __forceinline__ float2 scatter_ranges(R* r, int c8) {
 #pragma unroll
-  for (int o = kLanes / 2; o >= 1; o >>= 1) {
-    a = min_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
-    b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, o));
+  for (int o = 4; o >= 1; o >>= 1) {
+    const bool up = (c8 & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const R keep = up ? r[i + o] : r[i], give = up ? r[i] : r[i + o];
+      r[i] = range_join(keep, range_from(give, o));
+    }
   }
-  *mn = a;
-  *mx = b;
+  if (kLanes == 16) r[0] = range_join(r[0], range_from(r[0], 8));
+  return range_ends(r[0]);
 }
 
 __device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kKvqThreads, sizeof(T) == 2 ? 8 : 4) kvq_store
   constexpr KvqLayout Y = G::Y;
   constexpr int TT = G::TT, kLanes = G::kLanes, NR = G::NR, kT = G::kT, kRowsPass = G::kRowsPass, kPieces = G::kPieces;
   constexpr int kWords = Y.unit / 4;                     // words per V piece
-  static_assert(kLanes >= 2 * NR, "a lane for each row's parameters");
+  static_assert(2 * NR == 8 && (kLanes == 8 || kLanes == 16), "a lane for each row's parameters");
   __shared__ __align__(16) uint32_t s_va[G::kTiles * G::kVWords];
   __shared__ __align__(16) uint4 s_pa[G::kTiles * kPieces * D];
   pdl_wait();
@@ -308,19 +324,13 @@ __global__ void __launch_bounds__(kKvqThreads, sizeof(T) == 2 ? 8 : 4) kvq_store
         xv[k].load(static_cast<const T*>(p.v_src) + at);
       }
     }
-    // ranges of the 2 NR rows; then lane i of each row group works out the
-    // parameters of its i-th row, so that they cost one row's instructions
-    float mn = 0.f, mx = 0.f;
+    // lane i of each row group works out the parameters of its i-th row, so
+    // that they cost one row's instructions
+    decltype(range_of(xk[0])) part[2 * NR];
 #pragma unroll
-    for (int k = 0; k < 2 * NR; ++k) {
-      float a, e;
-      row_range<kLanes>(k < NR ? xk[k] : xv[k - NR], &a, &e);
-      if ((c8 & 7) == k) {
-        mn = a;
-        mx = e;
-      }
-    }
-    const KvqRow row = kvq_row<BITS>(mn, mx);
+    for (int k = 0; k < 2 * NR; ++k) part[k] = range_of(k < NR ? xk[k] : xv[k - NR]);
+    const float2 ends = scatter_ranges<kLanes>(part, c8);
+    const KvqRow row = kvq_row<BITS>(ends.x, ends.y);
     const int group = (tid & 31) & ~(kLanes - 1);
 #pragma unroll
     for (int k = 0; k < 2 * NR; ++k) {
