@@ -178,6 +178,7 @@ __device__ __noinline__ uint2 quantise8_exact(const Raw8<T> x, float z, float s)
 //   that, to a border, float64 decides.
 // Differences that overflow fail both tests. s is at most 2^-8 of itself below
 // (max - z) / (2^BITS - 1): n may reach 256 at 8 bits (held to 255), 15 at 4.
+// inv = 0 (equal values, or a row with NaN or infinity) gives zeros.
 template <typename T, int BITS>
 __device__ __forceinline__ void quantise8(const Raw8<T>& x, float z, float s, float inv, uint32_t* code, uint32_t* packed) {
   constexpr float kMagic = 12582912.f;                   // 1.5 * 2^23: rounds to the nearest whole, ties to even
@@ -209,11 +210,11 @@ __device__ __forceinline__ void quantise8(const Raw8<T>& x, float z, float s, fl
   for (int q = 0; q < 2; ++q)
     code[q] = __byte_perm(__byte_perm(b[4 * q], b[4 * q + 1], 0x0040), __byte_perm(b[4 * q + 2], b[4 * q + 3], 0x0040), 0x5410);
   if (kBf16 ? off != 0u : far > 0.5f - (BITS == 4 ? 0x1p-17f : 0x1p-14f)) {
-    const uint2 c = quantise8_exact<T, BITS>(x, z, s);
+    // (a row with NaN or infinity comes here too, and holds zeros)
+    const uint2 c = inv == 0.f ? make_uint2(0u, 0u) : quantise8_exact<T, BITS>(x, z, s);
     code[0] = c.x;
     code[1] = c.y;
   }
-  if (inv == 0.f) code[0] = code[1] = 0u;                // equal values, or a row with NaN or infinity
   if (BITS == 4) {
     const uint32_t lo = code[0] | (code[0] >> 4), hi = code[1] | (code[1] >> 4);   // two half-bytes a byte, at bytes 0 and 2
     *packed = __byte_perm(lo, hi, 0x6420);
@@ -331,6 +332,11 @@ __global__ void __launch_bounds__(kKvqThreads, sizeof(T) == 2 ? 8 : 4) kvq_store
     for (int k = 0; k < 2 * NR; ++k) part[k] = range_of(k < NR ? xk[k] : xv[k - NR]);
     const float2 ends = scatter_ranges<kLanes>(part, c8);
     const KvqRow row = kvq_row<BITS>(ends.x, ends.y);
+    if (c8 < 2 * NR) {
+      const int t = row0 + (c8 % NR) * kRowsPass;
+      if (t >= t0 && t < t1)
+        *reinterpret_cast<uint32_t*>(pg + (c8 < NR ? Y.off_kp : Y.off_vp) + (in_page + t) * 4) = pack_bf16x2(row.s, row.z);
+    }
     const int group = (tid & 31) & ~(kLanes - 1);
 #pragma unroll
     for (int k = 0; k < 2 * NR; ++k) {
@@ -340,8 +346,6 @@ __global__ void __launch_bounds__(kKvqThreads, sizeof(T) == 2 ? 8 : 4) kvq_store
       const float inv = __shfl_sync(0xffffffffu, row.inv, group + k);
       uint32_t code[2], packed = 0u;
       quantise8<T, BITS>(k < NR ? xk[k] : xv[k - NR], z, s, inv, code, &packed);
-      if (live && c8 == 0)
-        *reinterpret_cast<uint32_t*>(pg + (k < NR ? Y.off_kp : Y.off_vp) + (in_page + t) * 4) = pack_bf16x2(fabsf(s), z);
       if (k >= NR) {
         s_v[(t * kVStride<D>) / 4 + c8 * 2] = code[0];
         s_v[(t * kVStride<D>) / 4 + c8 * 2 + 1] = code[1];
