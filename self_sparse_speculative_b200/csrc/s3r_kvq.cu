@@ -11,7 +11,7 @@
 //   kvq_rollback_kernel  the lengths back to the committed prefix
 //
 // Measured (16 x 16384 tokens, 8 KV heads, D 128, 4 bits): quantising a bf16 cache
-// 386 us, 3.5 TB/s, bound by instruction issue (77% of cycles, 20 instructions a
+// 330 us, 4.1 TB/s, bound by instruction issue (73% of cycles, 17 instructions a
 // value); reading back 249 us, 5.5 TB/s, 0.83 of a copy's rate. Single rows are a
 // chain of dependent loads (length -> page id -> rows), 3 to 4 us a kernel.
 //
