@@ -1,0 +1,206 @@
+"""Attention over the quantised cache where the values' rows differ in kind and scale: rows of equal values (held with
+numbers that are all 0) that take much of the weight, rows a thousand times smaller or larger than their neighbours.
+
+The values of a head have a mean of +-1 (times the head's scale) a channel, so that outputs are as large as the values
+and the bound below is a small part of them. Bound of an output (u = 2^-24, N = 2^bits - 1, c = N / 2, p normalised
+weights, T positions; the sums over rows with numbers, `free` rows without):
+- the output's rounding, 2^-8 |out|; a score off by at most e = (32 + D / 4) u scale (s_k (N + 1) + |z_k|) sum |q| and the
+  exponential's 2^-21 move a weight by e' = e + 2^-21 + 4 u |score| of itself: sum p e' (|v| + |out|);
+- a query's smallest values are met with an error of at most 2^-22 (4 bits, up to 16 packed rows) or 2^-32 of the row's
+  largest: D of them times scale s_k N, added to e;
+- 4 bits, up to 16 packed rows: a weight w = p s_v is rounded to 9 bits, 2^-9 sum p |v|, and to whole steps of 2^-14
+  with the row's largest of at least 2^6: less than a step, N 2^-20 T max p s_v. Otherwise to float16: 2^-12 of itself and
+  2^-25 with the largest at least 2^8, against n - c: (c + 1) (2^-12 sum p s_v + 2^-33 T max p s_v). A row without numbers
+  has no s_v of its own; its weight is met as if its step were at most 2^-8 |z|: s_v = 2^-8 |z| in these sums;
+- sums in float32 over T positions: (T + 64) u (2 (N + 1) sum p s_v + sum p |v|), and with products that stand for
+  p z alone, off by 4 u each."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import oracle.kv_quant as Q                                                     # noqa: E402
+from self_sparse_speculative_b200 import s3r                                    # noqa: E402
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+U = 2.0 ** -24
+BIAS = 8.0                                                                     # every query's channel 0
+
+
+def bounded(q, held, n_v, scale, rows, bits, dtype):
+    """One sequence: out, lse and the bound of each output (module docstring). n_v [L, H, D]: the values' numbers."""
+    R, Hq, D = q.shape
+    L, H = held["sk"].shape
+    G, N = Hq // H, 2 ** bits - 1
+    e4 = dtype == "bf16" and bits == 4 and G * rows <= 16
+    out, lse, tol = np.zeros((R, Hq, D)), np.zeros((R, Hq)), np.zeros((R, Hq, D))
+    for h in range(H):
+        free = (n_v[:, h] == 0).all(-1)
+        sv = np.where(free, 2.0 ** -8 * np.abs(held["zv"][:, h]), held["sv"][:, h])
+        for r in range(R):
+            seen = np.arange(L) <= L - R + r
+            k, v, s = held["k"][seen, h], held["v"][seen, h], sv[seen]
+            T = len(v)
+            for g in range(G):
+                x = q[r, h * G + g].astype(np.float64)
+                y = k @ x * scale
+                p = np.exp(y - y.max())
+                lse[r, h * G + g] = y.max() + np.log(p.sum())
+                p /= p.sum()
+                o = p @ v
+                e = (32 + D / 4) * U * scale * (held["sk"][seen, h] * (N + 1) + np.abs(held["zk"][seen, h])) * np.abs(x).sum()
+                if dtype == "bf16":
+                    e = e + D * 2.0 ** (-22 if e4 else -32) * np.abs(x).max() * scale * N * held["sk"][seen, h]
+                e = e + 2.0 ** -21 + 4 * U * np.abs(y)
+                A, B, top = p @ np.abs(v), p @ s, (p * s).max()
+                t = (p * e) @ np.abs(v) + (p @ e) * np.abs(o) + (T + 64) * U * (2 * (N + 1) * B + A) + 4 * U * A
+                if dtype == "bf16":
+                    t = t + 2.0 ** -8 * np.abs(o)
+                    t = t + (2.0 ** -9 * A + N * 2.0 ** -20 * T * top if e4
+                             else (N / 2 + 1) * (2.0 ** -12 * B + 2.0 ** -33 * T * top))
+                out[r, h * G + g], tol[r, h * G + g] = o, 1.01 * t
+    return out, lse, tol
+
+
+class Cache:
+    """kinds[h](rng, v) turns the values [S, T, D] of head h, made with a mean of +-1 a channel, into what it needs."""
+
+    def __init__(self, lens, kinds, G, rows, D, P, bits, dtype, weight=None, seed=0):
+        rng = np.random.default_rng(seed)
+        S, H, T = len(lens), len(kinds), max(lens)
+        self.lens, self.rows, self.D, self.P, self.bits, self.dtype = lens, rows, D, P, bits, dtype
+        self.scale = D ** -0.5
+        width = -(-T // P)
+        self.table = rng.permutation(S * width).reshape(S, width).astype(np.int32)
+        k = rng.standard_normal((S, T, H, D)).astype(np.float32)
+        k[..., 0] = 0
+        if weight is not None:                              # position 1 takes about this weight of every row
+            k[:, 1] *= 0.01
+            k[:, 1, :, 0] = np.log(T * 1.13 * weight / (1 - weight)) / (BIAS * self.scale)
+        v = np.empty((S, T, H, D), dtype=np.float32)
+        mean = rng.choice([-1.0, 1.0], (H, D))
+        for h, kind in enumerate(kinds):
+            v[:, :, h] = kind(rng, mean[h] + 0.25 * rng.standard_normal((S, T, D)))
+        q = 0.5 * rng.standard_normal((S, rows, H * G, D)).astype(np.float32)
+        q[..., 0] = BIAS
+        self.q = torch.from_numpy(q).to(DT[dtype]).cuda()
+        self.pages = torch.zeros((S * width, H, Q.page_bytes(D, P, bits)), dtype=torch.uint8, device="cuda")
+        self.dlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        full = torch.zeros(S, dtype=torch.int32, device="cuda")
+        dtable = torch.from_numpy(self.table).cuda()
+        ws = torch.zeros(s3r.s3r_kv_workspace_bytes(S), dtype=torch.uint8, device="cuda")
+        writer = s3r.paged_kvq(self.pages, dtable, full, H * G, D, P, bits)     # (checked byte for byte elsewhere)
+        for a in range(0, T, 1024):
+            x, y = (torch.from_numpy(np.ascontiguousarray(z[:, a:a + 1024])).to(DT[dtype]).cuda() for z in (k, v))
+            s3r.s3r_kvq_append(writer, full, x, y, dtype, x.shape[1], 0, ws)
+        assert s3r.s3r_device_status(ws) == (0, 0)
+        self.kvq = s3r.paged_kvq(self.pages, dtable, self.dlens, H * G, D, P, bits)
+        self.out, self.lse = torch.zeros_like(self.q), torch.zeros((S, rows, H * G), device="cuda")
+        self.ws = torch.zeros(s3r.s3r_kvq_attn_workspace_bytes(self.kvq, dtype, rows), dtype=torch.uint8, device="cuda")
+
+    def call(self):
+        s3r.s3r_kvq_attn(self.kvq, self.q, self.dtype, self.rows, self.scale, self.out, self.lse, self.ws)
+
+    def numbers(self, b):
+        raw, n = self.pages.cpu().numpy(), -(-self.lens[b] // self.P)
+        return np.concatenate([np.stack([Q.read_page(raw[i, h], self.D, self.P, self.bits)[3] for h in range(raw.shape[1])], 1)
+                               for i in self.table[b, :n]])[:self.lens[b]]
+
+    def check(self, seqs):
+        raw = self.pages.cpu().numpy()
+        for b in seqs:
+            held = Q.held_rows(raw, self.table[b], self.lens[b], self.D, self.P, self.bits)
+            ref, lse, tol = bounded(self.q[b].float().cpu().numpy(), held, self.numbers(b), self.scale, self.rows, self.bits,
+                                    self.dtype)
+            out = self.out[b].double().cpu().numpy()
+            worst = np.abs(out - ref) - tol
+            G = out.shape[1] // raw.shape[1]
+            for h in range(raw.shape[1]):                   # head by head, so that a failure names its kind
+                o, r = out[:, h * G:(h + 1) * G], ref[:, h * G:(h + 1) * G]
+                l2 = np.linalg.norm(o - r) / (np.linalg.norm(r) + 1e-300)
+                assert (worst[:, h * G:(h + 1) * G] <= 1e-18).all(), (b, h, l2, tol[0, h * G, :3], r[0, 0, :3], o[0, 0, :3])
+            assert np.abs(self.lse[b].double().cpu().numpy() - lse).max() < 1e-3
+        assert s3r.s3r_device_status(self.ws) == (0, 0)
+
+
+def sink(value, scale):
+    """Position 1 holds one value in every channel; the others are `scale` times as large as usual."""
+    def kind(rng, v):
+        v = scale * v
+        v[:, 1] = value
+        return v
+    return kind
+
+
+def every_third(value, scale):
+    def kind(rng, v):
+        v = scale * v
+        v[:, ::3] = value
+        return v
+    return kind
+
+
+# packed rows of every form of the kernel: 4 and 16 of 4 bits, 20 and 45 of both widths, float32
+FORMS = [(4, 4, 1, "bf16"), (4, 4, 4, "bf16"), (4, 4, 5, "bf16"), (4, 5, 9, "bf16"), (8, 4, 1, "bf16"), (8, 5, 9, "bf16"),
+         (4, 4, 1, "f32")]
+KINDS = [sink(0.0, 1.0), sink(0.0, 0.05), sink(0.0, 1e-3), sink(1.0, 0.05), sink(-3.0, 1.0), sink(2.0 ** -10, 1.0),
+         every_third(0.0, 0.05), every_third(0.0, 1e-6), every_third(50.0, 1.0), every_third(0.0, 1e4)]
+
+
+@pytest.mark.parametrize("weight", [0.5, 0.99])
+@pytest.mark.parametrize("bits,G,rows,dtype", FORMS)
+def test_rows_of_equal_values_that_take_much_of_the_weight(bits, G, rows, dtype, weight):
+    c = Cache([3001, 700], KINDS, G, rows, 128, 64, bits, dtype, weight, seed=1)
+    c.call()
+    c.check([0, 1])
+
+
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 16), (64, 64)])
+@pytest.mark.parametrize("bits,G,rows", [(4, 4, 1), (4, 4, 5), (8, 4, 1), (8, 5, 9)])
+def test_rows_of_equal_values_in_the_other_layouts(D, P, bits, G, rows):
+    c = Cache([901, 333], KINDS, G, rows, D, P, bits, "bf16", 0.95, seed=2)
+    c.call()
+    c.check([0, 1])
+
+
+@pytest.mark.parametrize("bits,G,rows", [(4, 4, 1), (4, 4, 5), (8, 4, 1)])
+def test_units_of_one_cta(bits, G, rows):
+    # 160 (sequence, head) units: a CTA's references span whole sequences
+    c = Cache([2048] * 16, KINDS, G, rows, 128, 64, bits, "bf16", 0.99, seed=3)
+    c.call()
+    c.check([0, 15])
+
+
+@pytest.mark.parametrize("bits,G,rows,dtype", FORMS)
+def test_caches_of_equal_values_only(bits, G, rows, dtype):
+    c = Cache([200, 65], [every_third(0.0, 0.0), every_third(0.75, 0.0)], G, rows, 128, 64, bits, dtype, seed=4)
+    c.call()
+    c.check([0, 1])
+    assert (c.out[:, :, :G].float().abs() < 1e-15).all()
+
+
+def test_values_with_a_step_of_one():
+    # s = 1 with numbers, beside rows of equal values, which are held with s = 1 too: two values a row, 0 and 15 (255)
+    def steps(rng, v):
+        v = np.where(rng.random(v.shape) < 0.01, 15.0, 0.0)
+        v[:, ::2, 5] = 15.0
+        v[:, 3::4] = 0.0
+        return v
+    for bits in (4, 8):
+        for G, rows in ((4, 1), (5, 9)):
+            c = Cache([515, 64], [steps, lambda rng, v: 17.0 * steps(rng, v)], G, rows, 128, 64, bits, "bf16", 0.9, seed=5)
+            c.call()
+            c.check([0, 1])
+
+
+@pytest.mark.parametrize("bits,G,rows,dtype", FORMS)
+def test_long_sequences_with_a_bound_close_to_the_outputs(bits, G, rows, dtype):
+    # split over many CTAs and merged; a part lost or counted twice is far outside this bound
+    c = Cache([9001, 4097], [lambda rng, v: v, lambda rng, v: 0.05 * v], G, rows, 128, 64, bits, dtype, seed=6)
+    c.call()
+    c.check([0, 1])
