@@ -572,8 +572,11 @@ s3r_status s3r_kvq_rollback(const s3r_paged_kvq* kvq, int32_t* context_lens, con
  * q, out: [S, rows, Hq, D] in `dtype` (f32 or bf16), 16-byte aligned; lse:
  *   float32 [S, rows, Hq] or NULL.
  * Scores, softmax sums and outputs accumulate in float32. bf16: each weight
- *   p s_v is rounded once before it meets the values' whole numbers, to float16
- *   or (4 bits, up to 16 packed rows G * rows) to 9 significant bits; held values
+ *   p s_v (of a row without numbers: p |z| 2^-8) is rounded once before it meets the values' whole numbers.
+ *   4 bits and up to 16 packed rows (G * rows): to 9 significant bits, and to whole steps of
+ *   at most 2^-20 of the row's largest weight, up or down by thresholds that
+ *   vary with the position, so that the sum of many small weights is kept. Otherwise to float16:
+ *   11 bits, and steps of at most 2^-32 of the largest. Held values
  *   larger than 2^100 may overflow.
  * Supported as s3r_verify_attn: G <= 8, rows <= 17, G * rows <= 128.
  * workspace: s3r_kvq_attn_workspace_bytes(kvq, dtype, rows, budget_pages)

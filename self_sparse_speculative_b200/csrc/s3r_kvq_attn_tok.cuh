@@ -832,6 +832,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     uint8_t* const pw = E4 ? sP + (kpos & 15) : sP + kpos * 128;
     const int pck = E4 ? kpos >> 4 : kpos & 7;
     const uint32_t sign = E4 && (t & 1) ? 0x80008000u : 0u;   // every other token's weights are negated
+    // E4: weights below 2^-14 of the row's scale would all round to 0 (or all
+    // up), and 2^19 positions of 2^-21 of the largest are a quarter of it (such a
+    // row was off by 4.8%). So a weight is rounded after a token's own offset, 128 offsets
+    // spread evenly over a step of 2^-14, turned with the stage; t keeps its parity
+    // in them, since the numbers of odd tokens are complemented. A hidden weight of 0 stays 0.
+    auto offset_at = [&](uint32_t g) { return ((float)((uint32_t)(t * 79) + g * 54u & 127u) - 63.5f) * 0x1p-21f; };
 
     // barriers of a stage's products: S^T(x) complete; O^T with x's part complete
     auto s_done = [&](uint32_t x) { return mbar_wait(BAR(B_KE + x % NKE), (x / NKE) & 1, &s_abort, p.status); };
@@ -1004,6 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           tmem_wait_st();
         }
         uint8_t* const pb = pw + sb * L::kPBytes;
+        const float offset = E4 ? offset_at(g) : 0.f;
         uint32_t h[NR / 2];
 #pragma unroll
         for (int r = 0; r < NR; r += 2) {
@@ -1015,6 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           const float2 cn = fma_pair(w, both(zc), make_float2(corr[r], corr[r + 1]));
           corr[r] = cn.x;
           corr[r + 1] = cn.y;
+          if constexpr (E4) w = fma_pair(w, both(1.f), both(offset));
           h[r / 2] = half2_of(w.x, w.y);
           if constexpr (E4) {
             const Split sp = split2(h[r / 2] ^ sign);

@@ -9,7 +9,7 @@ weights, T positions; the sums over rows with numbers, `free` rows without):
 - a query's smallest values are met with an error of at most 2^-22 (4 bits, up to 16 packed rows) or 2^-32 of the row's
   largest: D of them times scale s_k N, added to e;
 - 4 bits, up to 16 packed rows: a weight w = p s_v is rounded to 9 bits, 2^-9 sum p |v|, and to whole steps of 2^-14
-  with the row's largest of at least 2^6: less than a step, N 2^-20 T max p s_v. Otherwise to float16: 2^-12 of itself and
+  with the row's largest of at least 2^6: by less than a step, N 2^-20 T max p s_v. Otherwise to float16: 2^-12 of itself and
   2^-25 with the largest at least 2^8, against n - c: (c + 1) (2^-12 sum p s_v + 2^-33 T max p s_v). A row without numbers
   has no s_v of its own; its weight is met as if its step were at most 2^-8 |z|: s_v = 2^-8 |z| in these sums;
 - sums in float32 over T positions: (T + 64) u (2 (N + 1) sum p s_v + sum p |v|), and with products that stand for
@@ -204,3 +204,69 @@ def test_long_sequences_with_a_bound_close_to_the_outputs(bits, G, rows, dtype):
     c = Cache([9001, 4097], [lambda rng, v: v, lambda rng, v: 0.05 * v], G, rows, 128, 64, bits, dtype, seed=6)
     c.call()
     c.check([0, 1])
+
+
+@pytest.mark.parametrize("bits,G,rows", [(4, 1, 1), (4, 4, 2), (4, 4, 4), (4, 4, 5), (8, 1, 1)])
+def test_many_weights_far_below_the_largest(bits, G, rows):
+    """524288 positions, the longest sequence, within one CTA (160 units over the same pages): two positions (one in
+    either half of the alternate stages) weigh 5 x 2^20 times as much as each other one, which so lies at a fifth of a
+    step of the narrow form's weights; together they have 5% of the weight.
+
+    Bound (norms over a head's outputs): the output's rounding 2^-8 |out|; two large weights rounded, 2^-9 sum p |v|; a weight goes up
+    or down to a whole step by thresholds that cover a step evenly over 128 positions (64 of either parity, whose
+    numbers are met differently): the mean is off by at most half a step in 64 positions, T 2^-27 N max p s_v, and the
+    numbers, drawn without regard to the position, vary by at most N / 2 around theirs, against errors of at most half
+    a step in the root mean square: six times sqrt(T) 2^-22 N max p s_v; the accumulator, rounded once for
+    32 positions (16 in float16) by at most 2^-23 of partial sums of at most (N + 1) sum p s_v; scores as in the
+    module docstring, below 1e-3 here."""
+    rng = np.random.default_rng(8)
+    S, H, D, P, width, pool = 80, 2, 128, 64, 8192, 256
+    T, N, scale = width * P, 2 ** bits - 1, 128 ** -0.5
+    k = 0.01 * rng.standard_normal((1, pool * P, H, D)).astype(np.float32)
+    k[..., 0] = 0
+    k[0, 1, :, 0] = np.log(5 * 2.0 ** 20) / (BIAS * scale)                     # page 0, listed twice
+    v = rng.choice([-1.0, 1.0], (H, D)) + 0.25 * rng.standard_normal((1, pool * P, H, D))
+    q = 0.01 * rng.standard_normal((S, rows, H * G, D)).astype(np.float32)
+    q[:] = q[:1]
+    q[..., 0] = BIAS
+    k, v, q = (torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda() for x in (k, v, q))
+    row = 1 + np.arange(width) % (pool - 1)
+    row[0] = row[2] = 0                                                        # positions 1 and 129
+    table = torch.from_numpy(np.tile(row, (S, 1)).astype(np.int32)).cuda()
+    pages = torch.zeros((pool, H, Q.page_bytes(D, P, bits)), dtype=torch.uint8, device="cuda")
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(s3r.s3r_kv_workspace_bytes(S), dtype=torch.uint8, device="cuda")
+    plain = torch.arange(pool, dtype=torch.int32, device="cuda")[None].contiguous()
+    writer = s3r.paged_kvq(pages, plain, lens, H * G, D, P, bits)
+    for a in range(0, pool * P, 1024):
+        s3r.s3r_kvq_append(writer, lens, k[:, a:a + 1024].contiguous(), v[:, a:a + 1024].contiguous(), "bf16", 1024, 0, ws)
+    full = torch.full((S,), T, dtype=torch.int32, device="cuda")
+    kvq = s3r.paged_kvq(pages, table, full, H * G, D, P, bits)
+    wa = torch.zeros(s3r.s3r_kvq_attn_workspace_bytes(kvq, "bf16", rows), dtype=torch.uint8, device="cuda")
+    out, lse = torch.zeros_like(q), torch.zeros((S, rows, H * G), device="cuda")
+    s3r.s3r_kvq_attn(kvq, q, "bf16", rows, scale, out, lse, wa)
+    assert s3r.s3r_device_status(ws) == (0, 0) and s3r.s3r_device_status(wa) == (0, 0)
+    held = Q.held_rows(pages.cpu().numpy(), np.arange(pool), pool * P, D, P, bits)
+    times = np.repeat(np.bincount(row, minlength=pool), P).astype(np.float64)
+    for b in (0, S - 1):
+        for h in range(H):
+            for r in range(rows):
+                for g in range(G):
+                    y = held["k"][:, h] @ q[b, r, h * G + g].double().cpu().numpy() * scale
+                    p = np.exp(y - y.max())
+                    # the last page, listed 32 times or more, ends the sequence: its last positions are hidden from the first rows
+                    n = times.copy()
+                    if r < rows - 1:
+                        n[row[-1] * P + P - (rows - 1 - r):row[-1] * P + P] -= 1
+                    w = n * p / (n * p).sum()
+                    one = p / (n * p).sum()
+                    ref, A = w @ held["v"][:, h], w @ np.abs(held["v"][:, h])
+                    top, B = (one * held["sv"][:, h]).max(), w @ held["sv"][:, h]
+                    tol = 2.0 ** -8 * np.abs(ref) + 1e-3 * A
+                    if bits == 4 and G * rows <= 16:
+                        tol = tol + 2.0 ** -9 * A + N * top * (T * 2.0 ** -27 + 6 * T ** 0.5 * 2.0 ** -22)
+                    else:
+                        tol = tol + (N / 2 + 1) * (2.0 ** -12 * B + 2.0 ** -33 * T * top)
+                    tol = tol + T / (32 if bits == 4 and G * rows <= 16 else 16) * 2.0 ** -23 * (N + 1) * B
+                    err = np.linalg.norm(out[b, r, h * G + g].double().cpu().numpy() - ref)
+                    assert err <= np.linalg.norm(tol), (b, h, r, g, err / np.linalg.norm(ref), np.linalg.norm(tol) / np.linalg.norm(ref))
