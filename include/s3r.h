@@ -568,7 +568,8 @@ s3r_status s3r_kvq_rollback(const s3r_paged_kvq* kvq, int32_t* context_lens, con
  *   without a list, else 1 to 8192.
  * A row that sees no position (only possible with a list) has out = 0 and lse
  * = -inf, as have all rows of a sequence with L_b < rows, L_b < 1 or
- * L_b > max_pages_per_seq * P (S3R_DEV_BAD_CONTEXT_LEN).
+ * L_b > max_pages_per_seq * P (S3R_DEV_BAD_CONTEXT_LEN). A row whose query holds NaN or an
+ * infinity and that sees a position has out and lse NaN.
  * q, out: [S, rows, Hq, D] in `dtype` (f32 or bf16), 16-byte aligned; lse:
  *   float32 [S, rows, Hq] or NULL.
  * Scores, softmax sums and outputs accumulate in float32. bf16: each weight

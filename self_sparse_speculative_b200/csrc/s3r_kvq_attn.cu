@@ -65,7 +65,9 @@ __global__ void __launch_bounds__(kF32Threads) kvq_attn_f32_kernel(const KvqAttn
   const float* q = static_cast<const float*>(p.q);
   for (int idx = tid; idx < rows * D; idx += kF32Threads) {
     const int i = idx / D, d = idx - (idx / D) * D;
-    sQ[idx] = q[kvq_out_row(p, b, h, i) * D + d];
+    // an infinite channel as NaN: scores of -inf alone would look like hidden ones
+    const float x = q[kvq_out_row(p, b, h, i) * D + d];
+    sQ[idx] = fabsf(x) < INFINITY ? x : __int_as_float(0x7fc00000);
     sO[idx] = 0.f;
   }
   for (int i = tid; i < rows; i += kF32Threads) {

@@ -804,7 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         const int ex = min(max((int)(__float_as_uint(big) >> 23), 40), 240);
         const float up = __uint_as_float((uint32_t)(254 - ex + 7) << 23);
         if (c8 == 0) {
-          s_qs[par][r] = sum;
+          // an infinite channel reaches every score as NaN: e4m3 would hold it as 448
+          s_qs[par][r] = big < INFINITY ? sum : __int_as_float(0x7fc00000);
           s_qf[par][r] = (E4 ? 512.f : 1.f) / up;
         }
 #pragma unroll
