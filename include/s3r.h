@@ -578,7 +578,8 @@ s3r_status s3r_kvq_rollback(const s3r_paged_kvq* kvq, int32_t* context_lens, con
  *   at most 2^-20 of the row's largest weight, up or down by thresholds that
  *   vary with the position, so that the sum of many small weights is kept. Otherwise to float16:
  *   11 bits, and steps of at most 2^-32 of the largest. Held values
- *   larger than 2^100 may overflow.
+ *   larger than 2^100 may overflow; scale: finite, below 2^111 in size (else
+ *   S3R_ERR_INVALID_ARG); queries keep their bits down to a row's largest value of 2^-103.
  * Supported as s3r_verify_attn: G <= 8, rows <= 17, G * rows <= 128.
  * workspace: s3r_kvq_attn_workspace_bytes(kvq, dtype, rows, budget_pages)
  *   bytes, zero-filled before first use.

@@ -535,7 +535,9 @@ S3R_EXPORT s3r_status s3r_kvq_attn(const s3r_paged_kvq* kvq, const void* q, s3r_
   p.budget = budget_pages;
   p.nsplit = pl.nsplit;
   p.chunk_pages = pl.chunk_pages;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  // bf16: the kernel's queries are met as 2^-16 of themselves
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634f * (dtype == S3R_BF16 ? 65536. : 1.));
+  if (!std::isfinite(p.scale_log2)) return S3R_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<uint32_t*>(w);
   p.tickets = reinterpret_cast<uint32_t*>(w + pl.off_tickets);

@@ -428,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   // parts' factors (-1: a part without tokens)
   __shared__ float s_xm[32], s_xl[32], s_f0[32], s_f1[32];
   __shared__ __align__(16) float s_corr[2][32];          // sum of w (z / s + c) per row
-  __shared__ __align__(16) float s_qs[2][64];            // by segment parity: sum of a query row
-  __shared__ __align__(16) float s_qf[2][64];            // 1 / the query row's scale
+  __shared__ __align__(16) float s_qs[2][64];            // by segment parity: 2^-16 of the sum of a query row
+  __shared__ __align__(16) float s_qf[2][64];            // 2^-16 / the query row's scale
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = (int)uni((uint32_t)tid >> 5);
@@ -792,24 +792,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         for (int i = 0; i < 4; ++i) {
           x[2 * i] = __uint_as_float(w[i] << 16);
           x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-          sum += x[2 * i] + x[2 * i + 1];
           big = fmaxf(big, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
         }
 #pragma unroll
-        for (int o = kDc / 2; o >= 1; o >>= 1) {
-          sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        }
-        // largest value into [128, 256)
-        const int ex = min(max((int)(__float_as_uint(big) >> 23), 40), 240);
+        for (int o = kDc / 2; o >= 1; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        // largest value into [128, 256), for values from 2^-103 to the type's
+        // largest (smaller ones keep fewer bits); 2^-16 / up and the token's 2^16
+        // scale stay in float32's range
+        const int ex = max((int)(__float_as_uint(big) >> 23), 24);
         const float up = __uint_as_float((uint32_t)(254 - ex + 7) << 23);
-        if (c8 == 0) {
-          // an infinite channel reaches every score as NaN: e4m3 would hold it as 448
-          s_qs[par][r] = big < INFINITY ? sum : __int_as_float(0x7fc00000);
-          s_qf[par][r] = (E4 ? 512.f : 1.f) / up;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          x[i] *= up;
+          x[i + 1] *= up;
+          sum += x[i] + x[i + 1];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= up;
+        for (int o = kDc / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (c8 == 0) {
+          const float back = 0x1p-16f / up;
+          // an infinite channel reaches every score as NaN: e4m3 would hold it as 448
+          s_qs[par][r] = big < INFINITY ? sum * back : __int_as_float(0x7fc00000);
+          s_qf[par][r] = (E4 ? 512.f : 1.f) * back;
+        }
         if constexpr (E4) {
           // 8 bytes at k = 8 c8: channels 0 2 4 6 1 3 5 7; hi and lo rows may differ in r & 7
           const Split a = split2(half2_of(x[0], x[2])), b = split2(half2_of(x[4], x[6]));

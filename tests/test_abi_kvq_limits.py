@@ -1,0 +1,25 @@
+"""Further refusals of the quantised cache's calls, on the host before any CUDA call (these run without a GPU)."""
+import ctypes
+
+import pytest
+
+from self_sparse_speculative_b200 import s3r
+
+FAKE = 0x10000   # a 16-byte-aligned non-null address; never dereferenced on these paths
+ARG, WS = s3r.S3R_ERR_INVALID_ARG, s3r.S3R_ERR_WORKSPACE
+
+
+def _kvq(**kw):
+    d = dict(num_seqs=2, num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=64, max_pages_per_seq=4,
+             num_pages_total=8, bits=4, pages=FAKE, block_table=FAKE, context_lens=FAKE)
+    d.update(kw)
+    c = s3r.PagedKVQ()
+    for k, v in d.items():
+        setattr(c, k, v)
+    return c
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 112, -2.0 ** 112, 3e38, float("nan"), float("inf")])
+def test_scales_that_leave_float32_are_refused(scale):
+    st = s3r.lib().s3r_kvq_attn(ctypes.byref(_kvq()), FAKE, s3r.S3R_BF16, 1, None, 0, scale, FAKE, None, FAKE, 1 << 40, None)
+    assert st == ARG

@@ -75,3 +75,15 @@ def test_a_query_that_is_not_finite_and_sees_nothing(bits, G, rows, dtype):
     assert out[0, :, :G].isnan().all() and lse[0, :, :G].isnan().all()
     assert (out[0, :, G:] == 0).all() and (lse[0, :, G:] == -float("inf")).all()
     assert torch.isfinite(out[1]).all()
+
+
+@pytest.mark.parametrize("shift", [-95, -40, 60, 113, 118, 125])
+@pytest.mark.parametrize("bits,G,rows,dtype", [f for f in FORMS if f[3] == "bf16"])
+def test_powers_of_two_move_between_query_and_scale(bits, G, rows, dtype, shift):
+    # q 2^shift with scale 2^-4 2^-shift (a power of two: exact in float32 down to 2^-149): every product moves by a
+    # power of two, so that the same bits come out. The largest queries, 3.5 x 2^125, are near the type's largest number.
+    q, call, _ = setup(bits, G, rows, dtype)
+    q = q.clamp(-3.5, 3.5)
+    out, lse = call(q, 0.0625)
+    o, l = call((q.float() * 2.0 ** shift).to(torch.bfloat16), 0.0625 * 2.0 ** -shift)
+    assert torch.equal(o, out) and torch.equal(l, lse)
