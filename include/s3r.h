@@ -40,10 +40,12 @@
  *   table, context lengths, logits) while the previous kernel on the stream
  *   is still finishing, when that kernel is one of this library's attention
  *   or sampling kernels (none of them writes another call's inputs;
- *   s3r_page_summaries, s3r_kv_append and s3r_kv_rollback, which do, let the
- *   next kernel start only when they are done). A kernel of the caller's
- *   that writes an input must not signal programmatic launch completion
- *   before that write.
+ *   s3r_page_summaries, s3r_kv_append, s3r_kv_rollback, s3r_kvq_append,
+ *   s3r_kvq_pack, s3r_kvq_read and s3r_kvq_rollback, which do, let the
+ *   next kernel start only when they are done). The calls on a quantised
+ *   cache (s3r_kvq_*) read nothing before the previous kernel is done. A
+ *   kernel of the caller's that writes an input must not signal programmatic
+ *   launch completion before that write.
  * - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *   stream). Work is enqueued asynchronously on it; outputs are ready when the
  *   stream reaches that point.
@@ -478,7 +480,8 @@ double s3r_round_cost_us(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, in
  *     V numbers  P*D*bits/8 bytes: [P*bits/8/u][D][u] with u = min(16, P*bits/8),
  *                byte j of piece c of channel d holds tokens c*8u/bits + j*8/bits ...
  *     V (s, z)   [P][2] bf16
- * block_table, context_lens: as in s3r_paged_kv; the two may be shared with a
+ * block_table, context_lens: as in s3r_paged_kv (every position below L_b has
+ *   been written by s3r_kvq_append or s3r_kvq_pack); the two may be shared with a
  *   s3r_paged_kv of the same sequences. A page that several sequences list may be written
  *   by one of them only, and in a call that no other sequence reads it in
  *   (copy before writing).

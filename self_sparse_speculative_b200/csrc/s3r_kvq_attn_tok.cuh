@@ -434,49 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = (int)uni((uint32_t)tid >> 5);
   pdl_launch_dependents();
-
-  if (warp == 0) {                                       // per-sequence prefix of unit pages
-    const int per = (p.S + 31) / 32;
-    const int b0 = min(p.S, lane * per), b1 = min(p.S, b0 + per);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += unit_pages(p, p.context_lens[b]) * p.Hkv;
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    int run = incl - sum;
-    for (int b = b0; b < b1; ++b) {
-      s_prefix[b] = run;
-      run += unit_pages(p, p.context_lens[b]) * p.Hkv;
-    }
-    if (lane == 31) s_prefix[p.S] = incl;
-  }
   if (tid < 64) s_roff[tid] = (tid / p.G) * p.Hq + (tid % p.G);
-  __syncthreads();
-  // inputs (cache, table, lengths, queries) may be read before the
-  // grid-dependency wait; page lists, outputs and the workspace only after it
-  if (blockIdx.x == 0) {
-    pdl_wait();
-    for (int b = 0; b < p.S; ++b) {
-      if (!kvq_bad_context(p, p.context_lens[b])) continue;
-      if (tid == 0) flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
-      for (int h = 0; h < p.Hkv; ++h) kvq_write_empty<__nv_bfloat16>(p, b, h, tid, kThreads);
-    }
-  }
-  const int total = (int)uni((uint32_t)s_prefix[p.S]);
-  // at least one stage of pages per CTA (shorter pieces would cost a merge
-  // for less than a stage); with lists, a whole unit per CTA where the units
-  // nearly fill the grid, so that none is split
-  int W = max((total + (int)gridDim.x - 1) / (int)gridDim.x, ppt);
-  if (p.page_list && W < p.budget && p.S * p.Hkv * 5 >= (int)gridDim.x * 4) W = p.budget;
-  const int lo = blockIdx.x * W, hi = min(total, lo + W);
-  if (lo >= hi) {                                        // uniform over the CTA
-    pdl_wait();
-    return;
-  }
-
   const uint32_t bar0 = smem_addr(&s_bar[0]);
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   // KF / VF: a stage's keys / values are unpacked in TMEM; TF: its token
@@ -487,15 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   // last waiter, so that none is two phases ahead of a wait.
   constexpr int B_FULL = 0, B_EMPTY = NS, B_KF = 2 * NS, B_VF = B_KF + NB, B_TF = B_VF + NB, B_KE = B_TF + kNT, B_VE = B_KE + NKE,
                 B_PF = B_VE + NB, B_QF = B_PF + NSB, B_TD = B_QF + 1, B_X = B_TD + 1, B_Y = B_X + 1;
-  uint8_t* sQ = dyn;
-  uint8_t* sP = dyn + L::kOffP;
-  uint8_t* sKV = dyn + L::kOffKV;
-  const uint32_t aQ = smem_addr(sQ), aP = smem_addr(sP), aKV = smem_addr(sKV);
-
-  if (warp == kMmaQk) {
-    tmem_alloc(smem_addr(&s_tmem), 512);
-    tmem_relinquish();
-  }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(BAR(B_FULL + i), 1);
@@ -517,6 +466,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     s_npend = 0;
     fence_barrier_init();
   }
+  // Everything below may have been written by the kernel before this one: a row
+  // just stored, a length just moved. That a writer lets this kernel launch only
+  // when it is done does not make its writes visible here; the wait does.
+  pdl_wait();
+  if (warp == 0) {                                       // per-sequence prefix of unit pages
+    const int per = (p.S + 31) / 32;
+    const int b0 = min(p.S, lane * per), b1 = min(p.S, b0 + per);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += unit_pages(p, p.context_lens[b]) * p.Hkv;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int run = incl - sum;
+    for (int b = b0; b < b1; ++b) {
+      s_prefix[b] = run;
+      run += unit_pages(p, p.context_lens[b]) * p.Hkv;
+    }
+    if (lane == 31) s_prefix[p.S] = incl;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int b = 0; b < p.S; ++b) {
+      if (!kvq_bad_context(p, p.context_lens[b])) continue;
+      if (tid == 0) flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
+      for (int h = 0; h < p.Hkv; ++h) kvq_write_empty<__nv_bfloat16>(p, b, h, tid, kThreads);
+    }
+  }
+  const int total = (int)uni((uint32_t)s_prefix[p.S]);
+  // at least one stage of pages per CTA (shorter pieces would cost a merge
+  // for less than a stage); with lists, a whole unit per CTA where the units
+  // nearly fill the grid, so that none is split
+  int W = max((total + (int)gridDim.x - 1) / (int)gridDim.x, ppt);
+  if (p.page_list && W < p.budget && p.S * p.Hkv * 5 >= (int)gridDim.x * 4) W = p.budget;
+  const int lo = blockIdx.x * W, hi = min(total, lo + W);
+  if (lo >= hi) return;                                  // uniform over the CTA
+
+  uint8_t* sQ = dyn;
+  uint8_t* sP = dyn + L::kOffP;
+  uint8_t* sKV = dyn + L::kOffKV;
+  const uint32_t aQ = smem_addr(sQ), aP = smem_addr(sP), aKV = smem_addr(sKV);
+
+  if (warp == kMmaQk) {
+    tmem_alloc(smem_addr(&s_tmem), 512);
+    tmem_relinquish();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -524,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
 
   if (warp == kProducer) {
     // ======================================================= producer warp
-    if (p.page_list) pdl_wait();
     const uint64_t pol = l2_policy_evict_first();
     // Pages in batches of 32 of one segment, a lane each: the lane that looked
     // a page up copies it, and the next batch's ids are in flight meanwhile.
@@ -536,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       if (p.page_list) there = there && *lp < (p.context_lens[s.b] + P - 1) / P;
       if (there) *ph = p.block_table[(size_t)s.b * p.max_pages + *lp];
     };
-    bool waited = p.page_list != nullptr, ok = true, more = true;
+    bool ok = true, more = true;
     uint32_t g = 0;
     int k = 0, lp, ph;
     Seg sg = locate_uni(p, s_prefix, lo, hi, W);
@@ -559,10 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       const uint8_t* const src = p.pages + ((size_t)max(ph, 0) * p.Hkv + sg.h) * Y.page_bytes;
       for (int j = 0; j < stages; ++j, ++g) {
         const uint32_t st = g % NS;
-        if (g == NS && !waited) {                        // the ring's first fill goes out before it
-          pdl_wait();
-          waited = true;
-        }
         if (!__all_sync(0xffffffffu, mbar_wait(BAR(B_EMPTY + st), ((g / NS) & 1) ^ 1, &s_abort, p.status))) {
           ok = false;
           break;
@@ -581,7 +573,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       lp = nlp;
       ph = nph;
     }
-    if (!waited) pdl_wait();
     // drain: wait until every issued copy has landed
     if (lane == 0)
       for (uint32_t k = g > NS ? g - NS : 0; k < g; ++k) mbar_wait_drain(BAR(B_FULL + k % NS), (k / NS) & 1, p.status);
@@ -859,8 +850,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
       else tmem_st8(at, x);
     };
     Seg sg = locate_uni(p, s_prefix, lo, hi, W);
-    q_prefetch(sg);                                      // an input: no earlier kernel writes it
-    pdl_wait();
     q_store(sg, 0);
     uint32_t g = 0;
     int seg = 0;
