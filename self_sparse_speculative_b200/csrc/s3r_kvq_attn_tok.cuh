@@ -489,9 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     if (lane == 31) s_prefix[p.S] = incl;
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
+  // sequences without pages have an unusable length
+  bool none = false;
+  if (blockIdx.x == 0)
+    for (int b = tid; b < p.S; b += kThreads) none |= s_prefix[b] == s_prefix[b + 1];
+  if (blockIdx.x == 0 && __syncthreads_or(none)) {
     for (int b = 0; b < p.S; ++b) {
-      if (!kvq_bad_context(p, p.context_lens[b])) continue;
+      if (s_prefix[b] != s_prefix[b + 1]) continue;
       if (tid == 0) flag_status(p.status, S3R_DEV_BAD_CONTEXT_LEN);
       for (int h = 0; h < p.Hkv; ++h) kvq_write_empty<__nv_bfloat16>(p, b, h, tid, kThreads);
     }

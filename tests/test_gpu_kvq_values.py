@@ -270,3 +270,23 @@ def test_many_weights_far_below_the_largest(bits, G, rows):
                     tol = tol + T / (32 if bits == 4 and G * rows <= 16 else 16) * 2.0 ** -23 * (N + 1) * B
                     err = np.linalg.norm(out[b, r, h * G + g].double().cpu().numpy() - ref)
                     assert err <= np.linalg.norm(tol), (b, h, r, g, err / np.linalg.norm(ref), np.linalg.norm(tol) / np.linalg.norm(ref))
+
+
+@pytest.mark.parametrize("bits,G,rows", [(4, 2, 2), (8, 5, 9)])
+def test_unusable_lengths_among_many_sequences(bits, G, rows):
+    # the first, the last and some between; more sequences than the kernel has threads
+    c = Cache([40] * 700, [lambda rng, v: v], G, rows, 64, 16, bits, "bf16", seed=9)
+    c.call()
+    ref, lse = c.out.clone(), c.lse.clone()
+    assert s3r.s3r_device_status(c.ws) == (0, 0)
+    bad = [0, 1, 31, 32, 350, 607, 608, 699]
+    c.dlens[bad] = torch.tensor([0, -1, rows - 1, 2 ** 31 - 1, -2 ** 31, 49, rows - 1, 0], dtype=torch.int32, device="cuda")
+    c.out.fill_(7.0)
+    c.lse.fill_(7.0)
+    c.call()
+    ref[bad], lse[bad] = 0.0, -float("inf")
+    assert torch.equal(c.out, ref) and torch.equal(c.lse, lse)
+    assert s3r.s3r_device_status(c.ws)[1] == s3r.S3R_DEV_BAD_CONTEXT_LEN
+    c.dlens.zero_()                                                            # no sequence has any page
+    c.call()
+    assert (c.out == 0).all() and (c.lse == -float("inf")).all()
