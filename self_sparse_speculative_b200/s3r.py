@@ -159,9 +159,11 @@ def dtype_code(dt) -> int:
 def paged_kv(k_cache, v_cache, block_table, context_lens, num_q_heads: int) -> PagedKV:
     """Describe a cache [num_pages_total, Hkv, P, D] with its block table."""
     n, h, p, d = k_cache.shape
-    return PagedKV(int(block_table.shape[0]), int(num_q_heads), int(h), int(d), int(p),
-                   int(block_table.shape[1]), int(n), dtype_code(k_cache.dtype),
-                   _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(context_lens))
+    kv = PagedKV(int(block_table.shape[0]), int(num_q_heads), int(h), int(d), int(p),
+                 int(block_table.shape[1]), int(n), dtype_code(k_cache.dtype),
+                 _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(context_lens))
+    kv.devices = {x.get_device() for x in (k_cache, v_cache, block_table, context_lens) if hasattr(x, "get_device")}
+    return kv
 
 
 def s3r_attn_workspace_bytes(kv: PagedKV, rows: int, budget_pages: int) -> int:
@@ -399,6 +401,10 @@ def s3r_kvq_pack(kv: PagedKV, kvq: PagedKVQ, last_n: int, workspace, workspace_b
     """Quantise the last last_n positions (0: all) of each sequence of kv into kvq."""
     wb = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
     device, _, _ = _kvq_env(None)
+    for at in getattr(kv, "devices", ()):
+        if at != device or at < 0:
+            raise ValueError(f"the source cache lives on {'the host' if at < 0 else f'cuda:{at}'}, "
+                             f"the current device is cuda:{device}")
     _same_device(device, kvq, workspace)
     st = _lib.s3r_kvq_pack(ctypes.byref(kv), ctypes.byref(kvq), int(last_n), _ptr(workspace), wb, _stream_on(stream, device))
     _check("s3r_kvq_pack", st)

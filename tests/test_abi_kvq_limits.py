@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from self_sparse_speculative_b200 import s3r
 
@@ -23,3 +24,20 @@ def _kvq(**kw):
 def test_scales_that_leave_float32_are_refused(scale):
     st = s3r.lib().s3r_kvq_attn(ctypes.byref(_kvq()), FAKE, s3r.S3R_BF16, 1, None, 0, scale, FAKE, None, FAKE, 1 << 40, None)
     assert st == ARG
+
+
+def test_packing_refuses_a_source_of_another_device():
+    k = torch.zeros((8, 2, 64, 128), dtype=torch.bfloat16)
+    table, lens = torch.zeros((2, 4), dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    kv = s3r.paged_kv(k, k, table, lens, 8)
+    assert kv.devices == {-1}
+    kvq, ws = _kvq(), FAKE
+    for at, name in (({0, 5}, "cuda:5"), ({0, -1}, "the host")):
+        kv.devices = at
+        current = s3r._kvq_env
+        s3r._kvq_env = lambda dtype: (0, None, None)                           # a process whose current device is cuda:0
+        try:
+            with pytest.raises(ValueError, match=f"source cache lives on {name}"):
+                s3r.s3r_kvq_pack(kv, kvq, 0, ws, workspace_bytes=4096, stream=0)
+        finally:
+            s3r._kvq_env = current
