@@ -59,6 +59,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -1207,10 +1208,14 @@ cudaError_t launch_one(const KvqAttnParams& p, cudaStream_t st) {
                                        (int)smem);
   if (e != cudaSuccess) return e;
   // the register split draws on the launch's registers: never run it on others
-  static const int regs = [] {
+  // (asked once; a query that fails is asked again by the next call)
+  static std::atomic<int> regs{0};
+  if (regs == 0) {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, attn_kernel<NR, ALT, D, P, BITS>) == cudaSuccess ? a.numRegs : 0;
-  }();
+    e = cudaFuncGetAttributes(&a, attn_kernel<NR, ALT, D, P, BITS>);
+    if (e != cudaSuccess) return e;
+    regs = a.numRegs;
+  }
   if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   int grid = device_sm_count();
   if (grid > kMaxPersistentCtas) grid = kMaxPersistentCtas;
