@@ -45,6 +45,8 @@ class DecodeStep:
     def __init__(self, wl: Workload, device="cuda", upload_chunk_pages: int = 2048, draft_bits: int | None = None):
         """draft_bits (4 or 8): also keep the cache in that many bits, for round_quantised()'s drafts."""
         self.wl = wl
+        if draft_bits not in (None, 4, 8):
+            raise ValueError(f"draft_bits is None, 4 or 8, got {draft_bits}")
         ws = wl.spec
         self.device = torch.device(device)
         dev = self.device
@@ -179,12 +181,18 @@ class DecodeStep:
         s3r.s3r_kv_rollback(self.kv, self.context_lens, self.num_accepted, R, self.kmin, self.kmax, self.ws_kv,
                             stream=stream)
 
+    def _need_copy(self):
+        if self.kvq is None:
+            raise ValueError("this step keeps no quantised copy of its cache: DecodeStep(..., draft_bits=4 or 8)")
+
     def quantise(self, last_n: int = 0, stream=None):
         """The cache's last last_n positions (0: all) into its quantised copy."""
+        self._need_copy()
         s3r.s3r_kvq_pack(self.kv, self.kvq, last_n, self.ws_kvq, stream=stream)
 
     def draft_quantised(self, i: int, stream=None):
         """Draft step i over every page of the quantised copy."""
+        self._need_copy()
         ws = self.wl.spec
         s3r.s3r_kvq_attn(self.kvq, self.q_draft[i].unsqueeze(1), ws.kv_dtype, 1, self.scale, self.draft_out[i].unsqueeze(1),
                          self.draft_lse[i].unsqueeze(1), self.ws_draft_q, stream=stream)
@@ -194,6 +202,7 @@ class DecodeStep:
         rows go to the copy and to the cache (the copy first: it takes the positions from the shared lengths),
         verification and sampling are those of every round, and the verifier's rows replace the drafter's in both.
         The copy holds the committed positions beforehand (quantise())."""
+        self._need_copy()
         ws = self.wl.spec
         g, R = ws.gamma, ws.rows
         st = torch.cuda.current_stream(self.device) if stream is None else stream
