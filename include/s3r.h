@@ -516,8 +516,8 @@ size_t s3r_kvq_page_bytes(int32_t head_dim, int32_t page_size, int32_t bits);
  * overwrite + n outside [1, max_pages_per_seq * P] is left unchanged
  * (S3R_DEV_BAD_CONTEXT_LEN); a row whose page id is out of range is not
  * written (S3R_DEV_BAD_PAGE_ID). Positions that are not written keep their
- * bits. workspace: s3r_kv_workspace_bytes(num_seqs) bytes, zero-filled before
- * first use.
+ * bits. workspace: s3r_kv_workspace_bytes(num_seqs) bytes, 4-byte aligned (else
+ * S3R_ERR_WORKSPACE), zero-filled before first use.
  */
 s3r_status s3r_kvq_append(const s3r_paged_kvq* kvq, int32_t* context_lens, const void* k_new, const void* v_new,
                           s3r_dtype dtype, int32_t n, int32_t overwrite, void* workspace, size_t workspace_bytes,
@@ -585,7 +585,7 @@ s3r_status s3r_kvq_rollback(const s3r_paged_kvq* kvq, int32_t* context_lens, con
  *   S3R_ERR_INVALID_ARG); queries keep their bits down to a row's largest value of 2^-103.
  * Supported as s3r_verify_attn: G <= 8, rows <= 17, G * rows <= 128.
  * workspace: s3r_kvq_attn_workspace_bytes(kvq, dtype, rows, budget_pages)
- *   bytes, zero-filled before first use.
+ *   bytes, 16-byte aligned (else S3R_ERR_WORKSPACE), zero-filled before first use.
  */
 size_t s3r_kvq_attn_workspace_bytes(const s3r_paged_kvq* kvq, s3r_dtype dtype, int32_t rows, int32_t budget_pages);
 s3r_status s3r_kvq_attn(const s3r_paged_kvq* kvq, const void* q, s3r_dtype dtype, int32_t rows,

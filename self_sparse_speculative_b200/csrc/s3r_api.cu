@@ -400,7 +400,9 @@ s3r_status check_kvq(const s3r_paged_kvq* c) {
 s3r_status check_kvq_call(const s3r_paged_kvq* c, const void* workspace, size_t workspace_bytes) {
   s3r_status s = check_kvq(c);
   if (s != S3R_OK) return s;
-  if (!workspace || workspace_bytes < kv_workspace_bytes(c->num_seqs)) return S3R_ERR_WORKSPACE;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 3u) != 0 ||   // counters of 4 bytes
+      workspace_bytes < kv_workspace_bytes(c->num_seqs))
+    return S3R_ERR_WORKSPACE;
   return S3R_OK;
 }
 
@@ -512,7 +514,7 @@ S3R_EXPORT s3r_status s3r_kvq_attn(const s3r_paged_kvq* kvq, const void* q, s3r_
   if (!q || !out || !aligned16(q) || !aligned16(out) || !std::isfinite(scale)) return S3R_ERR_INVALID_ARG;
   if ((page_list != nullptr) != (budget_pages > 0)) return S3R_ERR_INVALID_ARG;
   const AttnPlan pl = plan_kvq_attention(kvq, dtype, rows, budget_pages);
-  if (!workspace || workspace_bytes < pl.ws_bytes) return S3R_ERR_WORKSPACE;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < pl.ws_bytes) return S3R_ERR_WORKSPACE;   // partials of 16 bytes
   KvqAttnParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = q;

@@ -41,3 +41,15 @@ def test_packing_refuses_a_source_of_another_device():
                 s3r.s3r_kvq_pack(kv, kvq, 0, ws, workspace_bytes=4096, stream=0)
         finally:
             s3r._kvq_env = current
+
+
+def test_workspaces_off_their_alignment_are_refused():
+    lib, c, big, bf = s3r.lib(), _kvq(), 1 << 40, s3r.S3R_BF16
+    r, kv = ctypes.byref(c), s3r.PagedKV(2, 8, 2, 128, 64, 4, 8, bf, FAKE, FAKE, FAKE, FAKE)
+    for off in (1, 4, 8):                                                      # partial outputs are read 16 bytes at a time
+        assert lib.s3r_kvq_attn(r, FAKE, bf, 1, None, 0, 0.1, FAKE, None, FAKE + off, big, None) == WS
+    for off in (1, 2, 3):                                                      # counters of 4 bytes
+        assert lib.s3r_kvq_append(r, FAKE, FAKE, FAKE, bf, 1, 0, FAKE + off, big, None) == WS
+        assert lib.s3r_kvq_pack(ctypes.byref(kv), r, 0, FAKE + off, big, None) == WS
+        assert lib.s3r_kvq_read(r, None, 1, bf, FAKE, FAKE, FAKE + off, big, None) == WS
+        assert lib.s3r_kvq_rollback(r, FAKE, FAKE, 3, FAKE + off, big, None) == WS
