@@ -469,7 +469,8 @@ double s3r_round_cost_us(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, in
  * A row whose s would be below 2^-100 (equal values) has s = 1 and n = 0. A row that
  * holds NaN or an infinity has z = NaN: it reads back as NaN, and outputs of
  * the attention rows that see it are NaN; rows that do not see it are not
- * affected.
+ * affected. The same holds for a float32 row with a value below the lowest
+ * bf16 number (-3.39e38), which is held with z = -inf and s = inf.
  *
  * pages: [num_pages_total, Hkv, s3r_kvq_page_bytes(D, P, bits)] bytes, base
  *   16-byte aligned, of any content at first. The bytes of one (page, head):

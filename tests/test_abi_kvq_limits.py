@@ -53,3 +53,14 @@ def test_workspaces_off_their_alignment_are_refused():
         assert lib.s3r_kvq_pack(ctypes.byref(kv), r, 0, FAKE + off, big, None) == WS
         assert lib.s3r_kvq_read(r, None, 1, bf, FAKE, FAKE, FAKE + off, big, None) == WS
         assert lib.s3r_kvq_rollback(r, FAKE, FAKE, 3, FAKE + off, big, None) == WS
+
+
+def test_a_first_value_below_bf16_reads_as_nan():
+    # the definition's own rows: z rounds down to -inf, s = inf
+    import numpy as np
+    import oracle.kv_quant as Q
+    x = np.array([-3.4e38] + [0.0] * 63, dtype=np.float32)
+    with np.errstate(over="ignore", invalid="ignore"):
+        n, s, z = Q.quantise_rows(x, 4)
+        assert Q.bf16_value(z) == -np.inf and Q.bf16_value(s) == np.inf
+        assert np.isnan(Q.bf16_value(s) * 0.0 + Q.bf16_value(z))

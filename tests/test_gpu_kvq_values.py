@@ -290,3 +290,22 @@ def test_unusable_lengths_among_many_sequences(bits, G, rows):
     c.dlens.zero_()                                                            # no sequence has any page
     c.call()
     assert (c.out == 0).all() and (c.lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("bits,G,rows,dtype", FORMS)
+def test_a_float32_row_below_bf16_is_a_nan_row(bits, G, rows, dtype):
+    # its minimum rounds down to -inf: it reads back as NaN, and the rows that see it give NaN
+    c = Cache([130, 70], [lambda rng, v: v], G, rows, 128, 64, bits, dtype, seed=10)
+    c.call()
+    ref = c.out.clone()
+    x = torch.ones((2, 1, 1, 128), device="cuda")
+    x[1, 0, 0, 3] = -3.4e38
+    ws = torch.zeros(s3r.s3r_kv_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+    s3r.s3r_kvq_append(c.kvq, None, x, x, "f32", 1, 1, ws)                     # over the last position
+    out, val = torch.zeros_like(x), torch.zeros_like(x)
+    s3r.s3r_kvq_read(c.kvq, c.dlens - 1, 1, "f32", out, val, ws)
+    assert torch.equal(out[0], x[0]) and torch.equal(val[0], x[0]) and out[1].isnan().all() and val[1].isnan().all()
+    c.call()
+    assert c.out[1, rows - 1].isnan().all() and torch.equal(c.out[1, :rows - 1], ref[1, :rows - 1])
+    assert torch.isfinite(c.out[0]).all()
+    assert s3r.s3r_device_status(ws) == (0, 0) and s3r.s3r_device_status(c.ws) == (0, 0)
