@@ -130,15 +130,6 @@ __device__ __forceinline__ float2 scatter_ranges(R* r, int c8) {
   return range_ends(r[0]);
 }
 
-__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-
 template <typename T> __device__ __forceinline__ void store8(T* p, const float* x);
 template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
@@ -171,8 +162,9 @@ __device__ __noinline__ uint2 quantise8_exact(const Raw8<T> x, float z, float s)
 //   float32 unless the two are more than 2^16 apart: (x - z) + z tells where x
 //   is the small one (that sum is exact then), `wide` where z is (a row at a
 //   time; it reaches the lanes as the sign of s). The quotient corrected by its remainder is the exact one
-//   rounded: it equals a border m + 1/2 only if the quotient does (it is off a
-//   border by at least 2^-17 of itself otherwise).
+//   rounded: it equals a border m + 1/2 only if the quotient does. (Off a border, 2 (x - z) and s (2 m + 1)
+//   differ by a whole number of the smaller of their lowest bits; the first has 24 bits, the second at most 8 +
+//   BITS + 1, so they differ by more than 2^-24 of themselves, and float32 rounds by at most 2^-24.)
 // - float32: t = (x - z) (1 / s) is within 3 u t (u = 2^-24, t at most 2^BITS)
 //   of the exact quotient; nearer than 2^-17 (4 bits) or 2^-14 (8 bits), twice
 //   that, to a border, float64 decides.

@@ -10,7 +10,8 @@
 //   O^T[d, i] = sum_t (n_v[t, d] - c) w'[t, i]
 //   out       = (O^T + sum_t w (z_v[t] / s_v[t] + c)) / sum_t p
 // The reference of a row bounds y + log2 s_v, so that w stays in a narrow
-// type's range whatever the values' scales; queries are met as q 2^e with a
+// type's range whatever the values' scales (a row of equal values has no numbers for w to meet
+// and counts with a step of 2^-8 of its value); queries are met as q 2^e with a
 // power of two per row. Sums over tokens stay near zero (with n itself, or 16
 // + n, the accumulator's truncation built up an error of 1e-2 over 16384 tokens).
 //
@@ -25,7 +26,9 @@
 //   one spacing): 3 instructions for eight. Queries and weights are two terms hi +
 //   lo / 32 in separate columns, w rounded to 9 bits once for both its sums.
 //   Every other token's numbers are complemented (15 - n) and its weights
-//   negated, which keeps the sums over tokens near zero. The two terms cost the
+//   negated, which keeps the sums over tokens near zero. Below 2^-5 (the largest weight
+//   lies in 2^6 to 2^8) a weight has fewer bits, down to whole steps of 2^-14, taken up or down by a
+//   threshold of the token's own so that sums keep their value. The two terms cost the
 //   softmax 7 instructions a row and token: measured over 64 x 8192 tokens, 4
 //   rows take 568 ns a stage against 949 in f16, 8 rows 685 against 991, 16 rows 953
 //   against 1089; 24 rows were slower in it (1448 against 1385 ns, an earlier state of both).
@@ -220,14 +223,7 @@ __device__ __forceinline__ void unpack_e4(uint32_t w, uint32_t* r) {
   r[1] = ((w >> 4) ^ (ALT ? ~0u : 0u)) & 0x0f0f0f0fu;
 }
 
-// Two rows at once: d = a b + c, d = a b.
-__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
+// Two rows at once.
 __device__ __forceinline__ float2 mul_pair(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
@@ -235,7 +231,6 @@ __device__ __forceinline__ float2 mul_pair(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -316,13 +311,6 @@ __device__ __forceinline__ void warp_part(float* v, float (*red)[32], int q4, in
 }
 
 // Barrier over a softmax warpgroup (barriers 1 and 2).
-// Whether the phase of the given parity is complete, without suspending.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(r) : "r"(bar), "r"(parity) : "memory");
-  return r != 0u;
-}
 __device__ __forceinline__ void sync_wg(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
 // Number of its threads whose predicate is true.
 __device__ __forceinline__ int count_wg(int wg, bool pred) {
@@ -645,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
     const int t = tid & 127;                             // TMEM lane: token of S^T, channel of O^T
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
     constexpr int kWordsPage = P * BITS / 32;            // words of a channel in one page: 2, 4, 8 or 16
-      int Lb = -1, of = -1;                                // length of sequence `of`
+    int Lb = -1, of = -1;                                // length of sequence `of`
     // Words of a row (16-byte reads) to columns of this lane, 16 columns (8 bits:
     // 32) a turn of a rolled loop: five roles run on every SM quadrant at once and
     // instruction fetch, not arithmetic, bounds them (unrolled, 48 rows of 4-bit
@@ -885,10 +873,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         // passes under other work: with shared rows both before the parameters (48
         // rows: 1575 -> 1520 ns a stage); with alternate stages only PV(g - 2)'s, and
         // later, when it is likely done (8 rows 706 -> 685, at the top 718).
-        auto o_test = [&]() { return g < 2 || mbar_test(BAR(B_VE + (g - 2) % NB), ((g - 2) / NB) & 1); };
+        auto o_test = [&]() { return g < 2 || mbar_test_wait(BAR(B_VE + (g - 2) % NB), ((g - 2) / NB) & 1); };
         bool s_early = false, o_early = false;
         if (!ALT) {
-          s_early = mbar_test(BAR(B_KE + g % NKE), (g / NKE) & 1);
+          s_early = mbar_test_wait(BAR(B_KE + g % NKE), (g / NKE) & 1);
           o_early = o_test();
         }
         ok &= mbar_wait(BAR(B_TF + g % kNT), (g / kNT) & 1, &s_abort, p.status);
@@ -1018,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
           const float2 ln = fma_pair(w, both(rsv), make_float2(l[r], l[r + 1]));
           l[r] = ln.x;
           l[r + 1] = ln.y;
-          if constexpr (E4) w = round9(w);               // the numbers' and the minima's sums meet the same rounded weight
+          if constexpr (E4) w = round9(w);               // the numbers' and the minima's sums meet one rounded weight (small ones in the mean)
           const float2 cn = fma_pair(w, both(zc), make_float2(corr[r], corr[r + 1]));
           corr[r] = cn.x;
           corr[r + 1] = cn.y;
