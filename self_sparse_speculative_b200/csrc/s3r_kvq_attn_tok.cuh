@@ -696,9 +696,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         // weight to meet, so any step serves; one of about 2^-8 |z| keeps it
         // among its likes (2^-80: a row of zeros stays out of the way, and its
         // weights in float32's range). Its numbers tell it from a row whose step is 1.
-        // (Measured: 2% of a call; 16 x 16384 tokens whose values are all zero, 134 us instead of 66.)
-        if (valid && sv == 1.f && !any_number<D, BITS>(pg + Y.off_v, t % P, Y.unit))
-          put(__uint_as_float((uint32_t)max((int)(vp >> 23 & 0xffu) - 8, 47) << 23));
+        // The token's number is hidden from the compiler there, so that the addresses
+        // stay in the rare path (hoisted, 64 x 8192 tokens of 8 bits with one row took
+        // 210 us instead of 198). Sequences of zeros only pay for the search: twice a call's time.
+        if (valid && sv == 1.f) {
+          uint32_t u = (uint32_t)t;
+          asm volatile("" : "+r"(u));
+          if (!any_number<D, BITS>(stage + u / P * Y.page_bytes + Y.off_v, (int)(u % P), Y.unit))
+            put(__uint_as_float((uint32_t)max((int)(vp >> 23 & 0xffu) - 8, 47) << 23));
+        }
       };
       if (!E4 && uwg == 1) {
         // ahead of the values: the softmax needs them with S^T
