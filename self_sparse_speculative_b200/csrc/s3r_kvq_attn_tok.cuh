@@ -908,7 +908,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         if (!s_early) ok &= s_done(g);
         tc_fence_after();
         float s[NR];
-        // s <- y + log2 s_v (- reference); hidden: -inf
+        // s <- y + log2 s_v (- reference); hidden: -inf. The reference comes off the
+        // rounded sum, which is what it was raised from: taken off inside it, scores of
+        // 1e8 left weights beyond a float16 (infinite outputs) or none.
         auto load_s = [&](bool with_ref) {
           const uint32_t at = tmem + lane_base + L::kColS + g % NSB * N + rb;
           if constexpr (E4) {
@@ -939,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
             float4 nu = make_float4(0.f, 0.f, 0.f, 0.f);
             if (with_ref) nu = *reinterpret_cast<const float4*>(&s_nu[wg][r]);
             auto y = [&](float2 x, float2 f, float2 q, float2 n) {
-              return fma_pair(mul_pair(x, f), both(ka), fma_pair(q, both(kb), fma_pair(n, both(1.f), both(lgs))));
+              return fma_pair(fma_pair(mul_pair(x, f), both(ka), fma_pair(q, both(kb), both(lgs))), both(1.f), n);
             };
             const float2 a = y(make_float2(s[r], s[r + 1]), make_float2(qf.x, qf.y), make_float2(qs.x, qs.y), make_float2(nu.x, nu.y));
             const float2 b = y(make_float2(s[r + 2], s[r + 3]), make_float2(qf.z, qf.w), make_float2(qs.z, qs.w),
@@ -972,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
             const float mx = fmaxf(fmaxf(s_red[4 * wg][t], s_red[4 * wg + 1][t]),
                                    fmaxf(s_red[4 * wg + 2][t], s_red[4 * wg + 3][t]));
             const float m_old = -s_nu[wg][t];
-            const float m_new = fmaxf(m_old, mx - kTop);
+            const float m_new = fmaxf(m_old, __fsub_ru(mx, kTop));   // the largest weight is at most 2^kTop
             s_alpha[wg][t] = ex2(m_old - m_new);
             s_nu[wg][t] = -m_new;
           }

@@ -87,3 +87,40 @@ def test_powers_of_two_move_between_query_and_scale(bits, G, rows, dtype, shift)
     out, lse = call(q, 0.0625)
     o, l = call((q.float() * 2.0 ** shift).to(torch.bfloat16), 0.0625 * 2.0 ** -shift)
     assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e6, 1e8])
+@pytest.mark.parametrize("bits,G,rows,dtype", FORMS)
+def test_scores_that_float32_cannot_tell_apart(bits, G, rows, dtype, size):
+    """Scores up to about 1e10, where float32 is off by whole units: which of nearly equal positions win is open, but an
+    output is a weighted mean of held values whatever the weights. It lies between the least and the greatest of its
+    channel, up to the roundings of the weights (2^-9 of the largest value for the numbers and as much for the sum) and
+    of the output (2^-8)."""
+    S, H, D, P, lens = 2, 2, 128, 64, (2363, 517)
+    rng = np.random.default_rng(3)
+    width = -(-max(lens) // P)
+    new = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda()  # noqa: E731
+    k = new(S * width, H, P, D) * torch.exp(np.log(size) * torch.from_numpy(rng.random((S * width, H, P, 1)).astype(np.float32)).cuda())
+    k += 0.1 * size * new(S * width, H, P, 1)
+    v = new(S * width, H, P, D)
+    pages = torch.zeros((S * width, H, s3r.s3r_kvq_page_bytes(D, P, bits)), dtype=torch.uint8, device="cuda")
+    table = torch.arange(S * width, dtype=torch.int32, device="cuda").reshape(S, width)
+    full = torch.full((S,), width * P, dtype=torch.int32, device="cuda")
+    dlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kvq = s3r.paged_kvq(pages, table, dlens, H * G, D, P, bits)
+    ws = torch.zeros(s3r.s3r_kv_workspace_bytes(S), dtype=torch.uint8, device="cuda")
+    s3r.s3r_kvq_pack(s3r.paged_kv(k, v, table, full, H * G), kvq, 0, ws)
+    ko, held = torch.zeros((S, max(lens), H, D), device="cuda"), torch.zeros((S, max(lens), H, D), device="cuda")
+    s3r.s3r_kvq_read(kvq, None, max(lens), "f32", ko, held, ws)
+    wa = torch.zeros(s3r.s3r_kvq_attn_workspace_bytes(kvq, dtype, rows), dtype=torch.uint8, device="cuda")
+    assert s3r.s3r_device_status(ws) == (0, 0)
+    for seed in range(8):
+        q = (8 * new(S, rows, H * G, D)).to(DT[dtype])
+        out, lse = torch.zeros_like(q), torch.zeros((S, rows, H * G), device="cuda")
+        s3r.s3r_kvq_attn(kvq, q, dtype, rows, 0.1, out, lse, wa)
+        assert s3r.s3r_device_status(wa) == (0, 0)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        for b in range(S):
+            x = held[b, :lens[b]].repeat_interleave(G, 1)                      # [L, Hq, D]
+            tol = 2.0 ** -7 * x.abs().amax(0)
+            assert (out[b] <= x.amax(0) + tol).all() and (out[b] >= x.amin(0) - tol).all()
