@@ -29,9 +29,9 @@
 //   negated, which keeps the sums over tokens near zero. Below 2^-5 (the largest weight
 //   lies in 2^6 to 2^8) a weight has fewer bits, down to whole steps of 2^-14, taken up or down by a
 //   threshold of the token's own so that sums keep their value. The two terms cost the
-//   softmax 7 instructions a row and token: measured over 64 x 8192 tokens, 4
-//   rows take 568 ns a stage against 949 in f16, 8 rows 685 against 991, 16 rows 953
-//   against 1089; 24 rows were slower in it (1448 against 1385 ns, an earlier state of both).
+//   softmax about 8 instructions a row and token: 64 x 8192 tokens with 8 KV heads
+//   take 131 us a call at 4 rows against 230 in f16, 157 against 239 at 8, 218 against
+//   257 at 16, but 324 against 274 at 24.
 //
 // Both operands of numbers are the MMA's A operand (M = 128 tokens of S^T, M =
 // 128 lanes of channels of O^T) and live in tensor memory: a thread unpacks
@@ -50,11 +50,11 @@
 // over CTAs as in the bf16 attention (s3r_attn_sched.cuh), units shared by
 // several CTAs merge by log-sum-exp in the last one to finish.
 //
-// What bounds it, measured: HBM for few rows in 8 bits (64 x 8192 tokens, 8 KV heads, 1
-// to 4 rows: 6.3 TB/s, 0.96 of a copy's rate). Elsewhere instruction issue: five roles share
-// every SM quadrant, about 570 instructions a stage at 4 rows and 4 bits, issued in 53%
-// of cycles with instruction fetch among the first stalls (4.5 TB/s, 0.69;
-// 16 x 16384 tokens 67 us a call, 285 MB). 45 rows: 256 x 8192 tokens 1245 us, 1.9 TB/s: a
+// What bounds it, measured: HBM for few rows in 8 bits (64 x 8192 tokens, 8 KV heads, 4
+// packed rows: 6.2 TB/s, 0.94 of a copy's rate; 8: 0.86). Elsewhere instruction issue: five roles share
+// every SM quadrant, about 590 instructions a stage at 4 rows and 4 bits, issued in 53%
+// of cycles with instruction fetch among the first stalls (4.4 TB/s, 0.67;
+// 16 x 16384 tokens 70 us a call, 285 MB). 45 rows: 256 x 8192 tokens 1278 us, 1.8 TB/s: a
 // stage of the softmax warpgroups takes about 2300 cycles, 1300 of them scores and
 // weights, the rest the latencies of three waits, parameters and a barrier.
 #pragma once
@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
   const int total = (int)uni((uint32_t)s_prefix[p.S]);
   // at least one stage of pages per CTA (shorter pieces would cost a merge
   // for less than a stage); with lists, a whole unit per CTA where the units
-  // nearly fill the grid, so that none is split
+  // nearly fill the grid, so that none is split (a call of 120 units of 64 pages
+  // takes 24 us against 29 split, 128 of 32 pages 17 against 22, 144 of 64 pages 25 against 31)
   int W = max((total + (int)gridDim.x - 1) / (int)gridDim.x, ppt);
   if (p.page_list && W < p.budget && p.S * p.Hkv * 5 >= (int)gridDim.x * 4) W = p.budget;
   const int lo = blockIdx.x * W, hi = min(total, lo + W);
