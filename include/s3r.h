@@ -481,8 +481,8 @@ double s3r_round_cost_us(int32_t num_seqs, int32_t q_heads, int32_t kv_heads, in
  *     V numbers  P*D*bits/8 bytes: [P*bits/8/u][D][u] with u = min(16, P*bits/8),
  *                byte j of piece c of channel d holds tokens c*8u/bits + j*8/bits ...
  *     V (s, z)   [P][2] bf16
- * block_table, context_lens: as in s3r_paged_kv (every position below L_b has
- *   been written by s3r_kvq_append or s3r_kvq_pack); the two may be shared with a
+ * block_table, context_lens: as in s3r_paged_kv; every position below L_b has
+ *   been written by s3r_kvq_append or s3r_kvq_pack. The two may be shared with a
  *   s3r_paged_kv of the same sequences. A page that several sequences list may be written
  *   by one of them only, and in a call that no other sequence reads it in
  *   (copy before writing).
