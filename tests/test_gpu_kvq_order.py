@@ -86,3 +86,25 @@ def test_calls_behind_one_another(bits, dtype, G):
         graph.replay()
         assert all(torch.equal(x, y) for x, y in zip(c.held(), want))
     assert all(s3r.s3r_device_status(w) == (0, 0) for w in [c.ws] + c.wa)
+
+
+def test_calls_at_once_on_several_streams():
+    # chains over caches and workspaces of their own, on streams of their own at the same time
+    forms = [(4, "bf16", 4), (8, "bf16", 4), (4, "bf16", 8), (4, "f32", 2)]
+    chains = [Chain(*f) for f in forms]
+    want = []
+    for c in chains:
+        c.clear()
+        c.run(lambda: None)
+        want.append(c.held())
+    streams = [torch.cuda.Stream() for _ in chains]
+    for _ in range(3):
+        for c in chains:
+            c.clear()
+        for c, s in zip(chains, streams):
+            with torch.cuda.stream(s):
+                c.run(lambda: None)
+        torch.cuda.synchronize()
+        for c, w in zip(chains, want):
+            assert all(torch.equal(x, y) for x, y in zip(c.held(), w))
+    assert all(s3r.s3r_device_status(w) == (0, 0) for c in chains for w in [c.ws] + c.wa)
