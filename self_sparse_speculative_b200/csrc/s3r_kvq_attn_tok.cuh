@@ -700,11 +700,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         // The token's number is hidden from the compiler there, so that the addresses
         // stay in the rare path (hoisted, 64 x 8192 tokens of 8 bits with one row took
         // 210 us instead of 198). Sequences of zeros only pay for the search: twice a call's time.
-        if (valid && sv == 1.f) {
+        // A key of equal values scores scale z sum q: its centred numbers, -c s sum q, would
+        // cancel against c s sum q in float32 only, with s = 1 far above keys of small steps.
+        if (valid && (sv == 1.f || (kMid != 0.f && sk == 1.f))) {
           uint32_t u = (uint32_t)t;
           asm volatile("" : "+r"(u));
-          if (!any_number<D, BITS>(stage + u / P * Y.page_bytes + Y.off_v, (int)(u % P), Y.unit))
+          const uint8_t* const its = stage + u / P * Y.page_bytes;
+          if (sv == 1.f && !any_number<D, BITS>(its + Y.off_v, (int)(u % P), Y.unit))
             put(__uint_as_float((uint32_t)max((int)(vp >> 23 & 0xffu) - 8, 47) << 23));
+          if (kMid != 0.f && sk == 1.f) {
+            uint32_t any = 0u;
+#pragma unroll 1
+            for (uint32_t c = 0; c < D * BITS / 128; ++c) {
+              const uint4 w = *reinterpret_cast<const uint4*>(its + (c * P + u % P) * 16);
+              any |= w.x | w.y | w.z | w.w;
+            }
+            if (any == 0u) reinterpret_cast<float2*>(at4 + t)[0] = make_float2(0.f, p.scale_log2 * zk);
+          }
         }
       };
       if (!E4 && uwg == 1) {

@@ -32,8 +32,11 @@ U = 2.0 ** -24
 BIAS = 8.0                                                                     # every query's channel 0
 
 
-def bounded(q, held, n_v, scale, rows, bits, dtype):
-    """One sequence: out, lse and the bound of each output (module docstring). n_v [L, H, D]: the values' numbers."""
+def bounded(q, held, n_v, scale, rows, bits, dtype, n_k=None):
+    """One sequence: out, lse and the bound of each output (module docstring). n_v [L, H, D]: the values' numbers; n_k:
+    the keys' (a key without numbers has no s_k)."""
+    if n_k is not None:
+        held = dict(held, sk=np.where((n_k == 0).all(-1), 0.0, held["sk"]))
     R, Hq, D = q.shape
     L, H = held["sk"].shape
     G, N = Hq // H, 2 ** bits - 1
@@ -309,3 +312,32 @@ def test_a_float32_row_below_bf16_is_a_nan_row(bits, G, rows, dtype):
     assert c.out[1, rows - 1].isnan().all() and torch.equal(c.out[1, :rows - 1], ref[1, :rows - 1])
     assert torch.isfinite(c.out[0]).all()
     assert s3r.s3r_device_status(ws) == (0, 0) and s3r.s3r_device_status(c.ws) == (0, 0)
+
+
+@pytest.mark.parametrize("D,P", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("bits,G,rows,dtype", FORMS)
+def test_keys_of_equal_values_among_small_ones(bits, G, rows, dtype, D, P):
+    # every third key is zero or constant; the others a thousandth of usual, queries a thousand times: scores of size 1.
+    # A key without numbers scores scale z sum q, whatever step it is held with.
+    c = Cache([515, 130], [lambda rng, v: v] * 2, G, rows, D, P, bits, dtype, seed=11)
+    rng = np.random.default_rng(12)
+    k = 1e-3 * rng.standard_normal((2, 515, 2, D)).astype(np.float32)
+    k[:, ::3] = 0.0
+    k[:, 1::6] = 2.0 ** -12
+    k, v = (torch.from_numpy(x.astype(np.float32)).to(DT[dtype]).cuda() for x in (k, rng.standard_normal((2, 515, 2, D)) + 1.0))
+    lens = torch.full((2,), 515, dtype=torch.int32, device="cuda")
+    writer = s3r.paged_kvq(c.pages, torch.from_numpy(c.table).cuda(), lens, 2 * G, D, P, bits)
+    ws = torch.zeros(s3r.s3r_kv_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+    s3r.s3r_kvq_append(writer, None, k, v, dtype, 515, 515, ws)
+    c.q = (1e3 * torch.from_numpy(rng.standard_normal(c.q.shape).astype(np.float32)).cuda()).to(DT[dtype])
+    c.call()
+    assert s3r.s3r_device_status(ws) == (0, 0) and s3r.s3r_device_status(c.ws) == (0, 0)
+    raw = c.pages.cpu().numpy()
+    for b in range(2):
+        held = Q.held_rows(raw, c.table[b], c.lens[b], D, P, bits)
+        pages = [[Q.read_page(raw[i, h], D, P, bits) for h in range(2)] for i in c.table[b, :-(-c.lens[b] // P)]]
+        n_k, n_v = (np.concatenate([np.stack([x[j] for x in heads], 1) for heads in pages])[:c.lens[b]] for j in (0, 3))
+        ref, lse, tol = bounded(c.q[b].float().cpu().numpy(), held, n_v, c.scale, rows, bits, dtype, n_k)
+        out = c.out[b].double().cpu().numpy()
+        assert (np.abs(out - ref) <= tol).all(), (b, np.abs(out - ref).max(), tol.max())
+        assert np.abs(c.lse[b].double().cpu().numpy() - lse).max() < 1e-3      # e' of the docstring: at most 5e-4 here
