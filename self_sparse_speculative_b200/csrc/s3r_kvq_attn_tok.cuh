@@ -699,7 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const KvqAttnParams p
         // weights in float32's range). Its numbers tell it from a row whose step is 1.
         // The token's number is hidden from the compiler there, so that the addresses
         // stay in the rare path (hoisted, 64 x 8192 tokens of 8 bits with one row took
-        // 210 us instead of 198). Sequences of zeros only pay for the search: twice a call's time.
+        // 210 us instead of 198). A cache of equal rows only pays for the search: 16 x 16384
+        // tokens of zeros take 152 us back to back, others 66.
         // A key of equal values scores scale z sum q: its centred numbers, -c s sum q, would
         // cancel against c s sum q in float32 only, with s = 1 far above keys of small steps.
         if (valid && (sv == 1.f || (kMid != 0.f && sk == 1.f))) {
